@@ -20,7 +20,9 @@
  * FP8 quantisation pass.  Beyond that path: the fused quantise + GEMM forms
  * for decode, per-token and per-channel scales, the general (2N-2):2N
  * decomposition for N = 3 and 5, INT8 W8A8 and FP4 (quantisers and the
- * sparse GEMMs; each declared with its own citation below).
+ * sparse GEMMs; each declared with its own citation below), block-scaled FP4
+ * (quantiser and dense GEMM), and the norm and gated activation of a
+ * feed-forward block with quantised outputs.
  *
  * Conventions for every entry point
  * ---------------------------------
@@ -88,6 +90,10 @@ typedef struct CUstream_st *sp24_stream_t; /* identical to cudaStream_t */
 /* dtype codes */
 #define SP24_DTYPE_E4M3 0
 #define SP24_DTYPE_BF16 1
+
+/* block-scaled FP4 formats (fp4_quantize_microscaled and its kin) */
+#define SP24_FP4_NVFP4 0 /* blocks of 16, E4M3 scale each, one fp32 scale per row */
+#define SP24_FP4_MXFP4 1 /* blocks of 32, power-of-two scale each (E8M0 bytes) */
 
 /* op codes for sp24_workspace_size */
 #define SP24_OP_QUANTIZE 0
@@ -414,6 +420,92 @@ int sp24_prune_compress_perchannel(const void *W, int N, int K, uint8_t *values,
 int sp24_gemm_packed_scaled(const void *Xq, const float *x_scales, int x_per_token, const void *packed,
                             const float *w_scales, int w_per_channel, void *Y, int M, int N, int K,
                             void *workspace, size_t ws_bytes, int32_t *status, sp24_stream_t stream);
+
+/*
+ * Block-scaled FP4 (beyond the pages, whose FP4 has one scale per tensor; the
+ * SlideSparse summary names the precision, §3 "Contribuciones Clave").  Codes
+ * are E2M1 as above, two per byte, element 2i in the low nibble of byte i.
+ * Two formats:
+ *   SP24_FP4_NVFP4: per row R = max(amax, 2688 * 2^-100) and row_scale =
+ *     RN(R / 2688) (1 for an all-zero row); per block of 16 along the row sf =
+ *     E4M3(448 amax_b / R), code = E2M1(2688 x / (sf R)), 0 where sf = 0; both
+ *     quotients are rounded once, so ties are decided exactly.  An element
+ *     stands for code * sf * row_scale.
+ *   SP24_FP4_MXFP4: per block of 32, e = floor(log2 amax_b) - 2 and the scale
+ *     byte e + 127 (at least 0, and 0 for an all-zero block), code =
+ *     E2M1(x / 2^e), magnitudes above 6 saturate.  An element stands for
+ *     code * 2^(byte - 127).  No row scale: row_scales is not touched.
+ * Block scales lie in tiles of 128 rows by 4 scales, 512 bytes each, in the
+ * order the tensor cores read them: scale b of row r at byte
+ * ((r / 128) * ceil(n / 4) + b / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 +
+ * b % 4, n = cols / block.  Places outside the matrix hold zero bytes.
+ * fp4_block_scales_size: bytes of those tiles (0 for an unknown format or an
+ * empty matrix).
+ * fp4_quantize_microscaled: X bf16 [rows, cols] -> q u8 [rows, cols / 2],
+ *   block_scales, row_scales f32 [rows].  No workspace.  Shape rules: 1 <=
+ *   rows <= 2^31 - 128, cols % 32 == 0, 32 <= cols < 2^31.  Where a row holds
+ *   NaN/Inf, SP24_STATUS_NONFINITE is set and the outputs of that row (no
+ *   other) are unspecified.
+ * fp4_unpack_e4m3: the E4M3 codes (one byte each, exact) of FP4 codes: q u8
+ *   [rows, cols / 2] -> out u8 [rows, cols].  cols % 32 == 0.  With a
+ *   per-tensor scale that is an operand of the FP8 GEMMs.
+ */
+size_t fp4_block_scales_size(int64_t rows, int64_t cols, int format);
+int fp4_quantize_microscaled(const void *X, int64_t rows, int64_t cols, int format, uint8_t *q,
+                             uint8_t *block_scales, float *row_scales, int32_t *status, sp24_stream_t stream);
+int fp4_unpack_e4m3(const uint8_t *q, int64_t rows, int64_t cols, uint8_t *out, sp24_stream_t stream);
+
+/*
+ * The product of two block-scaled FP4 matrices of one format:
+ *   Y[m, n] = bf16( x_scale(m) * w_scale(n) * sum_k x[m, k] * w[n, k] ),
+ * x and w the values code * block scale, fp32 accumulation, x_scale(m) =
+ * x_scales[m] when x_per_token, else x_scales[0], or 1 when x_scales is NULL;
+ * w_scale(n) likewise.  Xq u8 [M, K / 2], Wq u8 [N, K / 2], block scales in
+ * the tiles above, of [M, K] and [N, K].  Y bf16 [M, N] must not alias an
+ * input.  No workspace; the same inputs give the same bits.  Shape rules:
+ * M >= 1, N % 8 == 0, K % 64 == 0, N >= 8, K >= 64.
+ */
+int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const float *x_scales, int x_per_token,
+                         const uint8_t *Wq, const uint8_t *w_block_scales, const float *w_scales, int w_per_channel,
+                         int format, void *Y, int M, int N, int K, int32_t *status, sp24_stream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition and a quantised output
+ * (the stage in front of an attention or feed-forward block; the SlideSparse
+ * summary fuses the per-token quantisation into the pass that makes the
+ * activations, §2 "Pipeline de Implementacion").
+ *   h = bf16(X + residual), or X when residual is NULL;
+ *   y = h * rsqrt(mean(h^2) + eps) * weight, fp32, the mean over the row.
+ * residual_out <- h (bf16 [rows, cols]; it may be X or residual itself, and
+ * is NULL exactly when residual is).  weight bf16 [cols].
+ * fp8_...: scales[m] = max(amax|y[m, :]| / 448, 2^-126) (1 for an all-zero
+ *   row), q u8 [rows, cols] = E4M3(y / scales[m]): an operand of
+ *   sp24_gemm_packed_scaled.  cols % 16 == 0.
+ * fp4_...: y quantised as fp4_quantize_microscaled quantises (cols % 32 == 0).
+ * No workspace.  SP24_STATUS_NONFINITE when a row holds NaN/Inf or its sum of
+ * squares leaves fp32's range; the outputs of that row alone are unspecified.
+ * SP24_ERR_SHAPE also for an eps that is negative or not finite.
+ */
+int fp8_rmsnorm_quantize_pertoken(const void *X, const void *residual, const void *weight, float eps, int64_t rows,
+                                  int64_t cols, void *residual_out, uint8_t *q, float *scales, int32_t *status,
+                                  sp24_stream_t stream);
+int fp4_rmsnorm_quantize_microscaled(const void *X, const void *residual, const void *weight, float eps,
+                                     int64_t rows, int64_t cols, int format, void *residual_out, uint8_t *q,
+                                     uint8_t *block_scales, float *row_scales, int32_t *status,
+                                     sp24_stream_t stream);
+
+/*
+ * The gated activation between the two products of a feed-forward block, with
+ * a quantised output.  GU bf16 [rows, 2 cols] holds the gate's columns, then
+ * the up projection's (one GEMM over both weights stacked); y = g / (1 +
+ * exp(-g)) * u in fp32, quantised as by the norm's two forms.  Shape rules,
+ * status and outputs as there.
+ */
+int fp8_silu_mul_quantize_pertoken(const void *GU, int64_t rows, int64_t cols, uint8_t *q, float *scales,
+                                   int32_t *status, sp24_stream_t stream);
+int fp4_silu_mul_quantize_microscaled(const void *GU, int64_t rows, int64_t cols, int format, uint8_t *q,
+                                      uint8_t *block_scales, float *row_scales, int32_t *status,
+                                      sp24_stream_t stream);
 
 /*
  * Dense FP8 GEMM of the same kernel family (comparison baseline for the

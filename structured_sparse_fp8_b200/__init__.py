@@ -11,7 +11,11 @@ Entry points (same names as the C ABI):
     sp24_prune_compress_packed, slide68_decompose_packed, sp24_gemm_packed,
     sp24_quantize_gemm_packed, slide68_lift_gemm_packed, fp8_quantize_pertoken,
     sp24_prune_compress_perchannel, sp24_gemm_packed_scaled, slide_decompose, slide_lift,
-    int8_quantize_pertensor, sp24_prune_compress_int8, sp24_gemm_int8_packed
+    int8_quantize_pertensor, sp24_prune_compress_int8, sp24_gemm_int8_packed,
+    fp4_quantize_pertensor, sp24_prune_compress_fp4, sp24_gemm_fp4,
+    fp4_quantize_microscaled, fp4_unpack_e4m3, fp4_gemm_microscaled,
+    fp8_rmsnorm_quantize_pertoken, fp4_rmsnorm_quantize_microscaled,
+    fp8_silu_mul_quantize_pertoken, fp4_silu_mul_quantize_microscaled
 """
 from __future__ import annotations
 
@@ -26,7 +30,10 @@ __all__ = [
     "sp24_gemm_packed", "sp24_quantize_gemm_packed", "slide68_lift_gemm_packed",
     "fp8_quantize_pertoken", "sp24_prune_compress_perchannel", "sp24_gemm_packed_scaled",
     "slide_decompose", "slide_lift", "int8_quantize_pertensor", "sp24_prune_compress_int8",
-    "sp24_gemm_int8_packed",
+    "sp24_gemm_int8_packed", "fp4_quantize_pertensor", "sp24_prune_compress_fp4", "sp24_gemm_fp4",
+    "fp4_quantize_microscaled", "fp4_unpack_e4m3", "fp4_gemm_microscaled", "fp4_block_scales_size",
+    "fp8_rmsnorm_quantize_pertoken", "fp4_rmsnorm_quantize_microscaled",
+    "fp8_silu_mul_quantize_pertoken", "fp4_silu_mul_quantize_microscaled",
     "Workspace",
     "Sp24Error", "DTYPE_E4M3", "DTYPE_BF16",
 ]
@@ -589,6 +596,223 @@ def fp8_gemm_dense(xq: torch.Tensor, x_scale, wq: torch.Tensor, w_scale,
                             _ptr(ws), wsn, _ptr(status), _stream(xq.device))
     _lib.check(rc, "fp8_gemm_dense")
     return y
+
+
+# ---------------------------------------------------------------------------
+# Block-scaled FP4, and the row stages of a block with quantised outputs
+# ---------------------------------------------------------------------------
+
+_FP4 = {"nvfp4": _lib.FP4_NVFP4, "mxfp4": _lib.FP4_MXFP4}
+_FP4_BLOCK = {"nvfp4": 16, "mxfp4": 32}
+
+
+def _fp4_format(format: str) -> int:
+    try:
+        return _FP4[format]
+    except (KeyError, TypeError):
+        raise Sp24Error(f"unknown FP4 format {format!r}: 'nvfp4' or 'mxfp4'") from None
+
+
+def _bf16_rows(t, name):
+    if t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise Sp24Error(f"{name} must be a 2-D bf16 tensor")
+    return t.shape
+
+
+def _operand(t, name, dtype, numel, device):
+    """An input or output of a call: the right type and size, contiguous, on the device of the call."""
+    if t.dtype != dtype or t.numel() != numel:
+        raise Sp24Error(f"{name} has the wrong shape or dtype")
+    if t.device != device or not t.is_contiguous():
+        raise Sp24Error(f"{name} must be contiguous and on {device}")
+    return t
+
+
+def _row_status(status, device):
+    return None if status is None else _operand(status, "status", torch.int32, 1, device).data_ptr()
+
+
+def _call(name, device, *args):
+    """One library call on `device`'s current stream, with that device current."""
+    fn = getattr(_lib.load(), name)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(device))
+    if rc:
+        _lib.check(rc, name)
+
+
+def fp4_block_scales_size(rows: int, cols: int, format: str = "nvfp4") -> int:
+    """Bytes of the block-scale tiles of a [rows, cols] matrix."""
+    block = _FP4_BLOCK[format] if _fp4_format(format) >= 0 else 0
+    return (rows + 127) // 128 * ((cols // block + 3) // 4) * 512
+
+
+def _fp4_outputs(rows, cols, format, device, out):
+    """(q, block_scales, row_scales) to write: those of ``out``, new ones where it has none."""
+    out = out or {}
+    size = fp4_block_scales_size(rows, cols, format)
+    q, blocks, scales = out.get("q"), out.get("block_scales"), out.get("row_scales")
+    q = (torch.empty((rows, cols // 2), dtype=torch.uint8, device=device) if q is None
+         else _operand(q, "q", torch.uint8, rows * (cols // 2), device))
+    blocks = (torch.empty(size, dtype=torch.uint8, device=device) if blocks is None
+              else _operand(blocks, "block_scales", torch.uint8, size, device))
+    if format == "mxfp4":
+        return q, blocks, None
+    scales = (torch.empty(rows, dtype=torch.float32, device=device) if scales is None
+              else _operand(scales, "row_scales", torch.float32, rows, device))
+    return q, blocks, scales
+
+
+def _fp8_outputs(rows, cols, device, out):
+    out = out or {}
+    q, scales = out.get("q"), out.get("scales")
+    q = (torch.empty((rows, cols), dtype=torch.uint8, device=device) if q is None
+         else _operand(q, "q", torch.uint8, rows * cols, device))
+    scales = (torch.empty(rows, dtype=torch.float32, device=device) if scales is None
+              else _operand(scales, "scales", torch.float32, rows, device))
+    return q, scales
+
+
+def fp4_quantize_microscaled(X: torch.Tensor, format: str = "nvfp4", status: torch.Tensor | None = None,
+                             out: dict | None = None):
+    """Block-scaled FP4 quantisation of X bf16 [rows, cols] (cols % 32 == 0).
+
+    format "nvfp4": blocks of 16 with E4M3 scales and one fp32 scale per row;
+    "mxfp4": blocks of 32 with power-of-two scales.  Returns (q u8 [rows,
+    cols / 2], block_scales u8 in the header's tile order, row_scales f32
+    [rows] or None for mxfp4); ``out`` may supply any of these preallocated.
+    """
+    _require_cuda(X)
+    fmt = _fp4_format(format)
+    rows, cols = _bf16_rows(X, "X")
+    dev = X.device
+    q, blocks, scales = _fp4_outputs(rows, cols, format, dev, out)
+    _call("fp4_quantize_microscaled", dev, X.data_ptr(), rows, cols, fmt, q.data_ptr(), blocks.data_ptr(),
+          _ptr(scales), _row_status(status, dev))
+    return q, blocks, scales
+
+
+def fp4_unpack_e4m3(q: torch.Tensor, out: torch.Tensor | None = None):
+    """The E4M3 codes (u8 [rows, cols], exact) of FP4 codes q u8 [rows, cols / 2]."""
+    _require_cuda(q)
+    if q.dtype != torch.uint8 or q.dim() != 2:
+        raise Sp24Error("q must be a 2-D uint8 tensor of packed FP4 codes")
+    rows, cols = q.shape[0], 2 * q.shape[1]
+    dev = q.device
+    o = (torch.empty((rows, cols), dtype=torch.uint8, device=dev) if out is None
+         else _operand(out, "out", torch.uint8, rows * cols, dev))
+    _call("fp4_unpack_e4m3", dev, q.data_ptr(), rows, cols, o.data_ptr())
+    return o
+
+
+def _row_scales(t, name, count, device):
+    """(pointer, one per row) of a scale argument: None, one value, or one per row."""
+    if t is None:
+        return None, 0
+    n = t.numel()
+    if n != 1 and n != count:
+        raise Sp24Error(f"{name} must hold one value or one per row")
+    return _operand(t, name, torch.float32, n, device).data_ptr(), int(n != 1)
+
+
+def fp4_gemm_microscaled(xq: torch.Tensor, x_block_scales: torch.Tensor, x_scales, wq: torch.Tensor,
+                         w_block_scales: torch.Tensor, w_scales, format: str = "nvfp4",
+                         out: torch.Tensor | None = None, status: torch.Tensor | None = None):
+    """Y bf16 [M, N] = x . w^T of two block-scaled FP4 matrices: xq u8 [M, K/2] and
+    wq u8 [N, K/2] with the block scales of fp4_quantize_microscaled; x_scales
+    and w_scales hold one value per row, one for all, or are None (1)."""
+    _require_cuda(xq)
+    fmt = _fp4_format(format)
+    if xq.dtype != torch.uint8 or xq.dim() != 2 or wq.dim() != 2:
+        raise Sp24Error("xq and wq must be 2-D uint8 tensors of packed FP4 codes")
+    m, n, k, dev = xq.shape[0], wq.shape[0], 2 * xq.shape[1], xq.device
+    _operand(wq, "wq", torch.uint8, n * (k // 2), dev)
+    _operand(x_block_scales, "x_block_scales", torch.uint8, fp4_block_scales_size(m, k, format), dev)
+    _operand(w_block_scales, "w_block_scales", torch.uint8, fp4_block_scales_size(n, k, format), dev)
+    xs, x_vec = _row_scales(x_scales, "x_scales", m, dev)
+    ws, w_vec = _row_scales(w_scales, "w_scales", n, dev)
+    y = (torch.empty((m, n), dtype=torch.bfloat16, device=dev) if out is None
+         else _operand(out, "out", torch.bfloat16, m * n, dev))
+    _call("fp4_gemm_microscaled", dev, xq.data_ptr(), x_block_scales.data_ptr(), xs, x_vec, wq.data_ptr(),
+          w_block_scales.data_ptr(), ws, w_vec, fmt, y.data_ptr(), m, n, k, _row_status(status, dev))
+    return y
+
+
+def _norm_inputs(X, weight, residual, residual_out):
+    _require_cuda(X)
+    rows, cols = _bf16_rows(X, "X")
+    dev = X.device
+    _operand(weight, "weight", torch.bfloat16, cols, dev)
+    if residual is None:
+        if residual_out is not None:
+            raise Sp24Error("residual_out needs a residual")
+        return rows, cols, dev, None
+    _operand(residual, "residual", torch.bfloat16, rows * cols, dev)
+    h = (torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if residual_out is None
+         else _operand(residual_out, "residual_out", torch.bfloat16, rows * cols, dev))
+    return rows, cols, dev, h
+
+
+def fp8_rmsnorm_quantize_pertoken(X: torch.Tensor, weight: torch.Tensor, eps: float,
+                                  residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                                  status: torch.Tensor | None = None, out: dict | None = None):
+    """Root-mean-square norm of h = X + residual with E4M3 output: returns (q u8
+    [rows, cols], scales f32 [rows], h bf16 [rows, cols]); without a residual h
+    is X itself.  residual_out may be X or residual (in place); ``out`` may
+    supply q and scales."""
+    rows, cols, dev, h = _norm_inputs(X, weight, residual, residual_out)
+    q, scales = _fp8_outputs(rows, cols, dev, out)
+    _call("fp8_rmsnorm_quantize_pertoken", dev, X.data_ptr(), _ptr(residual), weight.data_ptr(), eps, rows, cols,
+          _ptr(h), q.data_ptr(), scales.data_ptr(), _row_status(status, dev))
+    return q, scales, X if h is None else h
+
+
+def fp4_rmsnorm_quantize_microscaled(X: torch.Tensor, weight: torch.Tensor, eps: float, format: str = "nvfp4",
+                                     residual: torch.Tensor | None = None,
+                                     residual_out: torch.Tensor | None = None,
+                                     status: torch.Tensor | None = None, out: dict | None = None):
+    """Root-mean-square norm of h = X + residual with block-scaled FP4 output:
+    returns (q, block_scales, row_scales, h), the first three as
+    fp4_quantize_microscaled, h as fp8_rmsnorm_quantize_pertoken."""
+    fmt = _fp4_format(format)
+    rows, cols, dev, h = _norm_inputs(X, weight, residual, residual_out)
+    q, blocks, scales = _fp4_outputs(rows, cols, format, dev, out)
+    _call("fp4_rmsnorm_quantize_microscaled", dev, X.data_ptr(), _ptr(residual), weight.data_ptr(), eps, rows, cols,
+          fmt, _ptr(h), q.data_ptr(), blocks.data_ptr(), _ptr(scales), _row_status(status, dev))
+    return q, blocks, scales, X if h is None else h
+
+
+def _gated_rows(GU):
+    _require_cuda(GU)
+    rows, both = _bf16_rows(GU, "GU")
+    if both % 2:
+        raise Sp24Error("GU must hold as many gate as up columns")
+    return rows, both // 2, GU.device
+
+
+def fp8_silu_mul_quantize_pertoken(GU: torch.Tensor, status: torch.Tensor | None = None, out: dict | None = None):
+    """silu(gate) * up of GU bf16 [rows, 2 cols] (gate columns, then up columns)
+    with E4M3 output: returns (q u8 [rows, cols], scales f32 [rows])."""
+    rows, cols, dev = _gated_rows(GU)
+    q, scales = _fp8_outputs(rows, cols, dev, out)
+    _call("fp8_silu_mul_quantize_pertoken", dev, GU.data_ptr(), rows, cols, q.data_ptr(), scales.data_ptr(),
+          _row_status(status, dev))
+    return q, scales
+
+
+def fp4_silu_mul_quantize_microscaled(GU: torch.Tensor, format: str = "nvfp4", status: torch.Tensor | None = None,
+                                      out: dict | None = None):
+    """silu(gate) * up of GU bf16 [rows, 2 cols] with block-scaled FP4 output:
+    returns (q, block_scales, row_scales) as fp4_quantize_microscaled."""
+    fmt = _fp4_format(format)
+    rows, cols, dev = _gated_rows(GU)
+    q, blocks, scales = _fp4_outputs(rows, cols, format, dev, out)
+    _call("fp4_silu_mul_quantize_microscaled", dev, GU.data_ptr(), rows, cols, fmt, q.data_ptr(), blocks.data_ptr(),
+          _ptr(scales), _row_status(status, dev))
+    return q, blocks, scales
 
 
 def debug_e4m3_encode(v: torch.Tensor) -> torch.Tensor:

@@ -24,6 +24,8 @@ SP24_STATUS_NONFINITE = 1
 SP24_STATUS_TIMEOUT = 2
 DTYPE_E4M3 = 0
 DTYPE_BF16 = 1
+FP4_NVFP4 = 0
+FP4_MXFP4 = 1
 (OP_QUANTIZE, OP_PRUNE_COMPRESS, OP_SLIDE68_DECOMPOSE, OP_SLIDE68_LIFT, OP_GEMM, OP_GEMM_DENSE,
  OP_GEMM_PACKED, OP_QUANTIZE_GEMM_PACKED, OP_LIFT_GEMM_PACKED, OP_GEMM_FP4) = range(10)
 
@@ -31,6 +33,7 @@ _p = ctypes.c_void_p
 _i = ctypes.c_int
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
+_f = ctypes.c_float
 
 SIGNATURES = {
     "sp24_prune_compress": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _p, _sz, _p, _p]),
@@ -57,6 +60,14 @@ SIGNATURES = {
     "slide_lift": (_i, [_p, _i, _i, _i, _p, _p, _p, _sz, _p, _p]),
     "sp24_prune_compress_perchannel": (_i, [_p, _i, _i, _p, _p, _p, _p, _p]),
     "sp24_gemm_packed_scaled": (_i, [_p, _p, _i, _p, _p, _i, _p, _i, _i, _i, _p, _sz, _p, _p]),
+    "fp4_block_scales_size": (_sz, [_i64, _i64, _i]),
+    "fp4_quantize_microscaled": (_i, [_p, _i64, _i64, _i, _p, _p, _p, _p, _p]),
+    "fp4_unpack_e4m3": (_i, [_p, _i64, _i64, _p, _p]),
+    "fp4_gemm_microscaled": (_i, [_p, _p, _p, _i, _p, _p, _p, _i, _i, _p, _i, _i, _i, _p, _p]),
+    "fp8_rmsnorm_quantize_pertoken": (_i, [_p, _p, _p, _f, _i64, _i64, _p, _p, _p, _p, _p]),
+    "fp4_rmsnorm_quantize_microscaled": (_i, [_p, _p, _p, _f, _i64, _i64, _i, _p, _p, _p, _p, _p, _p]),
+    "fp8_silu_mul_quantize_pertoken": (_i, [_p, _i64, _i64, _p, _p, _p, _p]),
+    "fp4_silu_mul_quantize_microscaled": (_i, [_p, _i64, _i64, _i, _p, _p, _p, _p, _p]),
     "sp24_workspace_size": (_sz, [_i, _i64, _i64, _i64, _i]),
     "sp24_status_str": (ctypes.c_char_p, [_i]),
     "sp24_last_cuda_error": (_i, []),

@@ -16,8 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsp24.so")
-SOURCES = ["api.cu", "elementwise.cu", "fp4.cu", "gemm.cu", "int8.cu", "noalloc.cu", "rowscale.cu", "slide.cu", "smallx.cu",
-           "stream.cu"]
+SOURCES = ["api.cu", "elementwise.cu", "fp4.cu", "gemm.cu", "gemm_micro.cu", "int8.cu", "noalloc.cu",
+           "rowquant.cu", "rowscale.cu", "slide.cu", "smallx.cu", "stream.cu"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

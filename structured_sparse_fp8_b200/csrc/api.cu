@@ -6,6 +6,7 @@
 #include "fp4_kernels.h"
 #include "int8_kernels.h"
 #include "kernels.h"
+#include "micro_kernels.h"
 #include "sp24.h"
 
 namespace {
@@ -515,6 +516,130 @@ int fp8_gemm_dense(const uint8_t *Xq, const float *x_scale, const uint8_t *Wq,
                    size_t ws_bytes, int32_t *status, sp24_stream_t stream) {
   return gemm_common(sp24::kDenseE4M3, Xq, x_scale, Wq, nullptr, w_scale, Y, M, N, K, workspace,
                      ws_bytes, status, stream);
+}
+
+// ---- block-scaled FP4, and the row stages with quantised outputs
+
+static int fp4_block(int format) { return format == SP24_FP4_NVFP4 ? 16 : format == SP24_FP4_MXFP4 ? 32 : 0; }
+
+size_t fp4_block_scales_size(int64_t rows, int64_t cols, int format) {
+  const int block = fp4_block(format);
+  if (!block || rows < 1 || cols < block || cols % block != 0) return 0;
+  return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>((cols / block + 3) / 4) * 512;
+}
+
+// format < 0: E4M3 codes with a scale per row.
+enum RowStage { kStagePlain, kStageNorm, kStageGate };
+static int rowquant_common(RowStage stage, int format, sp24::RowQuantArgs a, sp24_stream_t stream) {
+  const bool fp8 = format < 0;
+  if (!fp8 && !fp4_block(format)) return SP24_ERR_DTYPE;
+  const bool row_scale = fp8 || format == SP24_FP4_NVFP4;
+  if (!a.x || !a.q || (!fp8 && !a.blocks) || (row_scale && !a.scales)) return SP24_ERR_NULL;
+  if (stage == kStageNorm && (!a.weight || (a.residual == nullptr) != (a.residual_out == nullptr))) return SP24_ERR_NULL;
+  const int mult = fp8 ? 16 : 32;
+  if (a.rows < 1 || a.rows > INT32_MAX - 127ll || a.cols < mult || a.cols % mult != 0 || a.cols > INT32_MAX)
+    return SP24_ERR_SHAPE;
+  if (stage == kStageNorm && !(a.eps >= 0.0f && a.eps <= 3.402823466e38f)) return SP24_ERR_SHAPE;
+  if (!aligned16(a.x) || !aligned16(a.q) || !aligned16(a.residual) || !aligned16(a.residual_out) ||
+      !aligned16(a.weight) || (!fp8 && !aligned16(a.blocks)) || (row_scale && !aligned16(a.scales)))
+    return SP24_ERR_ALIGN;
+  if (device_sm_count() < 0) return SP24_ERR_ARCH;
+  const sp24::RowOut out = fp8 ? sp24::kOutE4M3 : format == SP24_FP4_NVFP4 ? sp24::kOutNvfp4 : sp24::kOutMxfp4;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(stage == kStagePlain  ? sp24::launch_rowquant_plain(out, a, st)
+                     : stage == kStageNorm ? sp24::launch_rowquant_norm(out, a, st)
+                                           : sp24::launch_rowquant_gate(out, a, st));
+}
+
+static sp24::RowQuantArgs rowquant_args(const void *x, int64_t rows, int64_t cols, uint8_t *q, uint8_t *blocks,
+                                        float *scales, int32_t *status) {
+  sp24::RowQuantArgs a{};
+  a.x = static_cast<const uint16_t *>(x);
+  a.rows = rows;
+  a.cols = cols;
+  a.q = q;
+  a.blocks = blocks;
+  a.scales = scales;
+  a.status = status;
+  return a;
+}
+
+int fp4_quantize_microscaled(const void *X, int64_t rows, int64_t cols, int format, uint8_t *q,
+                             uint8_t *block_scales, float *row_scales, int32_t *status, sp24_stream_t stream) {
+  if (format < 0) return SP24_ERR_DTYPE;
+  return rowquant_common(kStagePlain, format, rowquant_args(X, rows, cols, q, block_scales, row_scales, status), stream);
+}
+
+int fp4_unpack_e4m3(const uint8_t *q, int64_t rows, int64_t cols, uint8_t *out, sp24_stream_t stream) {
+  if (!q || !out) return SP24_ERR_NULL;
+  if (rows < 1 || rows > INT32_MAX || cols < 32 || cols % 32 != 0 || cols > INT32_MAX) return SP24_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(out)) return SP24_ERR_ALIGN;
+  if (device_sm_count() < 0) return SP24_ERR_ARCH;
+  return cuda_status(sp24::launch_fp4_unpack(q, rows * (cols / 2), out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int fp8_rmsnorm_quantize_pertoken(const void *X, const void *residual, const void *weight, float eps, int64_t rows,
+                                  int64_t cols, void *residual_out, uint8_t *q, float *scales, int32_t *status,
+                                  sp24_stream_t stream) {
+  sp24::RowQuantArgs a = rowquant_args(X, rows, cols, q, nullptr, scales, status);
+  a.residual = static_cast<const uint16_t *>(residual);
+  a.weight = static_cast<const uint16_t *>(weight);
+  a.residual_out = static_cast<uint16_t *>(residual_out);
+  a.eps = eps;
+  return rowquant_common(kStageNorm, -1, a, stream);
+}
+
+int fp4_rmsnorm_quantize_microscaled(const void *X, const void *residual, const void *weight, float eps,
+                                     int64_t rows, int64_t cols, int format, void *residual_out, uint8_t *q,
+                                     uint8_t *block_scales, float *row_scales, int32_t *status,
+                                     sp24_stream_t stream) {
+  if (format < 0) return SP24_ERR_DTYPE;
+  sp24::RowQuantArgs a = rowquant_args(X, rows, cols, q, block_scales, row_scales, status);
+  a.residual = static_cast<const uint16_t *>(residual);
+  a.weight = static_cast<const uint16_t *>(weight);
+  a.residual_out = static_cast<uint16_t *>(residual_out);
+  a.eps = eps;
+  return rowquant_common(kStageNorm, format, a, stream);
+}
+
+int fp8_silu_mul_quantize_pertoken(const void *GU, int64_t rows, int64_t cols, uint8_t *q, float *scales,
+                                   int32_t *status, sp24_stream_t stream) {
+  return rowquant_common(kStageGate, -1, rowquant_args(GU, rows, cols, q, nullptr, scales, status), stream);
+}
+
+int fp4_silu_mul_quantize_microscaled(const void *GU, int64_t rows, int64_t cols, int format, uint8_t *q,
+                                      uint8_t *block_scales, float *row_scales, int32_t *status,
+                                      sp24_stream_t stream) {
+  if (format < 0) return SP24_ERR_DTYPE;
+  return rowquant_common(kStageGate, format, rowquant_args(GU, rows, cols, q, block_scales, row_scales, status), stream);
+}
+
+int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const float *x_scales, int x_per_token,
+                         const uint8_t *Wq, const uint8_t *w_block_scales, const float *w_scales, int w_per_channel,
+                         int format, void *Y, int M, int N, int K, int32_t *status, sp24_stream_t stream) {
+  const int block = fp4_block(format);
+  if (!block) return SP24_ERR_DTYPE;
+  if (!Xq || !x_block_scales || !Wq || !w_block_scales || !Y) return SP24_ERR_NULL;
+  if (M < 1 || N < 8 || N % 8 != 0 || K < 64 || K % 64 != 0) return SP24_ERR_SHAPE;
+  if (!aligned16(Xq) || !aligned16(x_block_scales) || !aligned16(Wq) || !aligned16(w_block_scales) || !aligned16(Y) ||
+      !aligned16(x_scales) || !aligned16(w_scales))
+    return SP24_ERR_ALIGN;
+  if (device_sm_count() < 0) return SP24_ERR_ARCH;
+  sp24::MicroGemmArgs a{};
+  a.xq = Xq;
+  a.xb = x_block_scales;
+  a.wq = Wq;
+  a.wb = w_block_scales;
+  a.xs = x_scales;
+  a.ws = w_scales;
+  a.x_vec = x_per_token ? 1 : 0;
+  a.w_vec = w_per_channel ? 1 : 0;
+  a.y = static_cast<uint16_t *>(Y);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.status = status;
+  return cuda_status(sp24::launch_micro_gemm(block, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int sp24_debug_e4m3_encode(const float *v, uint8_t *out, int64_t n, sp24_stream_t stream) {

@@ -1,0 +1,602 @@
+"""Block-scaled FP4 (quantiser, unpacking, product), the quantising norm and
+gated activation, against the float64 oracle.
+
+The quantiser of bf16 values is bit-exact.  Behind the norm and the activation
+the values that are quantised carry fp32 rounding errors of a known relative
+size d, so a code must lie between the codes of the reference value times
+(1 - d) and (1 + d) under the kernel's own scales, and the scales likewise.
+The product is held to half a bf16 step plus the fp32 accumulation's error.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import micro_oracle as MO
+from oracle import sp24_oracle as O
+from structured_sparse_fp8_b200 import workloads as WL
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+U = 2.0 ** -24   # half an fp32 step
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(DEV)
+
+
+def sp():
+    import structured_sparse_fp8_b200 as m
+    return m
+
+
+def dev_bf16(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16).to(DEV)
+
+
+def bits_of(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def unpack(b):
+    b = b.cpu().numpy()
+    out = np.empty((b.shape[0], 2 * b.shape[1]), dtype=np.uint8)
+    out[:, 0::2], out[:, 1::2] = b & 0xF, b >> 4
+    return out
+
+
+def pack(codes):
+    return (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)
+
+
+def rows_of(blocks, rows, cols, fmt):
+    """Scale bytes [rows, n]; everything else in the tiles must be zero."""
+    n = cols // MO.BLOCK[fmt]
+    t = blocks.cpu().numpy()
+    assert t.size == MO.tile_bytes(rows, n)
+    byts = MO.from_tiles(t, rows, n)
+    assert np.array_equal(MO.to_tiles(byts), t), "a scale outside the matrix is not zero"
+    return byts
+
+
+# ------------------------------------------------------------------ quantiser
+QSHAPES = [(1, 32), (1, 4096), (3, 64), (7, 96), (127, 160), (128, 256), (129, 1056), (300, 4096), (5, 16416),
+           (2, 40000), (3000, 64), (2, 131072)]
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("shape", QSHAPES)
+def test_quantize_bit_exact(fmt, shape):
+    for i, (dist, scale) in enumerate((("normal", 1.0), ("student_t3", 0.02), ("ties", 1.0))):
+        x = WL.random_bits(shape, 4000 + 10 * shape[1] + i, scale=scale, dist=dist)
+        if shape[0] > 2:
+            x[1] = 0                                        # an all-zero row
+            x[2, :16] = 0                                   # and an empty block
+        st = status()
+        q, blocks, rs = sp().fp4_quantize_microscaled(dev_bf16(x), fmt, status=st)
+        torch.cuda.synchronize()
+        codes, byts, ref_rs = MO.quantize(O.bf16_to_f32(x).astype(np.float64), fmt)
+        assert int(st.item()) == 0
+        assert np.array_equal(rows_of(blocks, *shape, fmt), byts)
+        assert np.array_equal(unpack(q), codes)
+        if fmt == "nvfp4":
+            assert np.array_equal(rs.cpu().numpy(), ref_rs)
+        else:
+            assert rs is None
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_quantize_every_finite_bf16_value(fmt):
+    """Rows that hold every finite bf16 value in some block, beneath row
+    maxima from a subnormal to the largest finite value."""
+    bits = np.arange(65536, dtype=np.uint16)
+    v = O.bf16_to_f32(bits)
+    for top in (0x0001, 0x0100, 0x1400, 0x3F80, 0x4195, 0x7F7F):
+        limit = O.bf16_to_f32(np.array([top], dtype=np.uint16))[0]
+        keep = bits[np.isfinite(v) & (np.abs(v) <= limit)]
+        flat = np.random.default_rng(top).permutation(keep)
+        cols = 1024
+        rows = -(-flat.size // (cols - 1))
+        x = np.full((rows, cols), top, dtype=np.uint16)
+        body = np.zeros(rows * (cols - 1), dtype=np.uint16)
+        body[:flat.size] = flat
+        x[:, 1:] = body.reshape(rows, cols - 1)
+        st = status()
+        q, blocks, rs = sp().fp4_quantize_microscaled(dev_bf16(x), fmt, status=st)
+        codes, byts, ref_rs = MO.quantize(O.bf16_to_f32(x).astype(np.float64), fmt)
+        assert int(st.item()) == 0
+        assert np.array_equal(rows_of(blocks, rows, cols, fmt), byts), hex(top)
+        assert np.array_equal(unpack(q), codes), hex(top)
+        if fmt == "nvfp4":
+            assert np.array_equal(rs.cpu().numpy(), ref_rs), hex(top)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("bad", [0x7F80, 0xFF80, 0x7FC0])
+def test_quantize_flags_nonfinite_rows_and_keeps_the_others(fmt, bad):
+    for shape in ((4, 64), (4, 20000)):
+        x = WL.random_bits(shape, 77)
+        codes, byts, _ = MO.quantize(O.bf16_to_f32(x).astype(np.float64), fmt)
+        y = x.copy()
+        y[2, shape[1] - 3] = bad
+        st = status()
+        q, blocks, _ = sp().fp4_quantize_microscaled(dev_bf16(y), fmt, status=st)
+        assert int(st.item()) == sp()._lib.SP24_STATUS_NONFINITE
+        keep = [0, 1, 3]
+        assert np.array_equal(unpack(q)[keep], codes[keep])
+        assert np.array_equal(rows_of(blocks, *shape, fmt)[keep], byts[keep])
+
+
+@pytest.mark.parametrize("shape", [(1, 32), (3, 96), (17, 4096), (1000, 1056)])
+def test_unpack_is_exact(shape):
+    codes = np.random.default_rng(shape[1]).integers(0, 16, shape).astype(np.uint8)
+    out = sp().fp4_unpack_e4m3(torch.from_numpy(pack(codes)).to(DEV))
+    assert out.shape == shape
+    want = O.e4m3_encode(O.e2m1_decode(codes).astype(np.float32))
+    assert np.array_equal(out.cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ norm, gate
+def between(got, lo, hi, what):
+    ok = (got >= lo) & (got <= hi)
+    assert ok.all(), f"{what}: {int((~ok).sum())} of {ok.size} outside; first at {np.argwhere(~ok)[:3].tolist()}"
+
+
+def check_e4m3(q, s, y, d):
+    """E4M3 codes and row scales of values y (float64) known to relative d."""
+    q, s = q.cpu().numpy(), s.cpu().numpy().astype(np.float64)
+    d = np.broadcast_to(d, y.shape)
+    top = np.abs(y).max(axis=1)
+    dr = d.max(axis=1) + 2 * U
+    between(s, MO.e4m3_row_scale(top * (1 - dr)), MO.e4m3_row_scale(top * (1 + dr)), "row scale")
+    t = np.abs(y) / s[:, None]
+    got = np.abs(O.e4m3_decode(q))
+    between(got, O.e4m3_decode(O.e4m3_encode((t * (1 - d - 4 * U)).astype(np.float32))),
+            O.e4m3_decode(O.e4m3_encode((t * (1 + d + 4 * U)).astype(np.float32))), "code")
+    nz = got > 0
+    assert np.array_equal(np.signbit(O.e4m3_decode(q))[nz], np.signbit(y)[nz])
+
+
+def check_fp4(q, blocks, rs, y, d, fmt):
+    rows, cols = y.shape
+    codes, byts = unpack(q), rows_of(blocks, rows, cols, fmt)
+    d = np.broadcast_to(d, y.shape)
+    n = cols // MO.BLOCK[fmt]
+    top = np.abs(y).reshape(rows, n, -1).max(axis=2)
+    db = d.reshape(rows, n, -1).max(axis=2) + 2 * U
+    sv = MO.scale_values(byts, fmt)
+    if fmt == "nvfp4":
+        amax, dr = top.max(axis=1), d.max(axis=1) + 2 * U
+        between(rs.cpu().numpy().astype(np.float64), MO.nvfp4_row_scale(amax * (1 - dr)) * (1 - U),
+                MO.nvfp4_row_scale(amax * (1 + dr)) * (1 + U), "row scale")
+        R = np.where(amax == 0, MO.ROW_FLOOR, rs.cpu().numpy().astype(np.float64) * 2688.0)
+        t = 448.0 * top / R[:, None]
+        lo, hi = ((t * (1 + sg * (db + 6 * U))).astype(np.float32) for sg in (-1, 1))
+        between(sv, O.e4m3_decode(O.e4m3_encode(lo)), O.e4m3_decode(O.e4m3_encode(hi)), "block scale")
+        many = np.repeat(sv, 16, axis=1) * R[:, None] / 2688.0
+    else:
+        assert rs is None
+        between(byts.astype(int), MO.mxfp4_block_bytes(top * (1 - db)).astype(int),
+                MO.mxfp4_block_bytes(top * (1 + db)).astype(int), "block scale")
+        many = np.repeat(sv, 32, axis=1)
+    t = np.where(many > 0, np.abs(y) / np.where(many > 0, many, 1.0), 0.0)
+    got = np.abs(O.e2m1_decode(codes))
+    lo, hi = (O.e2m1_decode(MO.e2m1_codes(t * (1 + sg * (d + 8 * U)))) for sg in (-1, 1))
+    between(got, lo, hi, "code")
+    nz = got > 0
+    assert np.array_equal((codes & 8 != 0)[nz], np.signbit(y)[nz])
+
+
+def norm_error(cols):
+    """Relative error of y: the fp32 sum of squares (in any order over 32
+    threads or more: cols / 32 + 16 additions deep, halved by the root), the
+    mean, eps, the root and the two products."""
+    return (cols / 64 + 16) * U
+
+
+NSHAPES = [(1, 32), (1, 4096), (5, 64), (130, 96), (64, 4096), (3, 8192), (4, 11008), (2, 16416), (2, 70016)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("shape", NSHAPES)
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm(fmt, shape, residual):
+    rows, cols = shape
+    x = WL.random_bits(shape, 5000 + cols, scale=2.0)
+    r = WL.random_bits(shape, 5001 + cols, scale=3.0) if residual else None
+    w = WL.random_bits((1, cols), 5002 + cols)[0]
+    if rows > 3:
+        x[3] = 0
+        if residual:
+            r[3] = 0
+    eps = 1e-5
+    y, h = MO.rmsnorm(x, r, w, eps)
+    st = status()
+    X, W, R = dev_bf16(x), dev_bf16(w), (dev_bf16(r) if residual else None)
+    if fmt == "e4m3":
+        q, s, hk = sp().fp8_rmsnorm_quantize_pertoken(X, W, eps, residual=R, status=st)
+        check_e4m3(q, s, y, norm_error(cols))
+    else:
+        q, b, s, hk = sp().fp4_rmsnorm_quantize_microscaled(X, W, eps, fmt, residual=R, status=st)
+        check_fp4(q, b, s, y, norm_error(cols), fmt)
+    assert int(st.item()) == 0
+    assert np.array_equal(bits_of(hk), h)
+    assert np.array_equal(bits_of(X), x)
+    if residual:
+        assert np.array_equal(bits_of(R), r)
+    else:
+        assert hk is X
+
+
+@pytest.mark.parametrize("where", ["x", "residual"])
+@pytest.mark.parametrize("cols", [64, 4096, 30000 // 32 * 32])
+def test_norm_in_place(where, cols):
+    x, r = WL.random_bits((9, cols), 61), WL.random_bits((9, cols), 62)
+    w = dev_bf16(WL.random_bits((1, cols), 63)[0])
+    q0, s0, h0 = sp().fp8_rmsnorm_quantize_pertoken(dev_bf16(x), w, 1e-6, residual=dev_bf16(r))
+    X, R = dev_bf16(x), dev_bf16(r)
+    target = X if where == "x" else R
+    q, s, h = sp().fp8_rmsnorm_quantize_pertoken(X, w, 1e-6, residual=R, residual_out=target)
+    assert h is target
+    assert torch.equal(h, h0) and torch.equal(q, q0) and torch.equal(s, s0)
+
+
+def test_norm_of_a_zero_row_without_eps_and_with_a_zero_weight():
+    x = WL.random_bits((2, 96), 5)
+    x[1] = 0
+    w = WL.random_bits((1, 96), 6)[0]
+    w[:64] = 0
+    st = status()
+    y, _ = MO.rmsnorm(x, None, w, 0.0)
+    q, s, _ = sp().fp8_rmsnorm_quantize_pertoken(dev_bf16(x), dev_bf16(w), 0.0, status=st)
+    check_e4m3(q, s, y, norm_error(96))
+    # zeros of the sign of 0 * weight
+    assert s[1].item() == 1.0 and not (q[1] & 0x7F).any()
+    for fmt in ("nvfp4", "mxfp4"):
+        q, b, s, _ = sp().fp4_rmsnorm_quantize_microscaled(dev_bf16(x), dev_bf16(w), 0.0, fmt, status=st)
+        check_fp4(q, b, s, y, norm_error(96), fmt)
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("bad", [0x7F80, 0x7FC0, 0x7F00])  # Inf, NaN, and a square beyond fp32
+def test_norm_flags_nonfinite_rows_and_keeps_the_others(bad):
+    for cols in (96, 20000):
+        x = WL.random_bits((5, cols), 8)
+        w = WL.random_bits((1, cols), 9)[0]
+        good_q, good_s, _ = sp().fp8_rmsnorm_quantize_pertoken(dev_bf16(x), dev_bf16(w), 1e-5)
+        x[1, 17] = bad
+        st = status()
+        q, s, _ = sp().fp8_rmsnorm_quantize_pertoken(dev_bf16(x), dev_bf16(w), 1e-5, status=st)
+        assert int(st.item()) == sp()._lib.SP24_STATUS_NONFINITE
+        keep = [0, 2, 3, 4]
+        assert torch.equal(q[keep], good_q[keep]) and torch.equal(s[keep], good_s[keep])
+
+
+GSHAPES = [(1, 32), (1, 11008), (5, 64), (130, 96), (64, 1056), (7, 14336), (3, 33024)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("shape", GSHAPES)
+def test_gate(fmt, shape):
+    rows, cols = shape
+    gu = WL.random_bits((rows, 2 * cols), 6000 + cols, scale=2.0)
+    gu[:, 5] = 0xC2C8                                       # a gate of -100: 0
+    gu[:, 6] = 0x42C8                                       # and of 100
+    gu[:, 7] = 0                                            # and of 0
+    if rows > 3:
+        gu[3] = 0
+    y = MO.silu_mul(gu)
+    # the exponential is off by 2 + 1.173 |g| steps at most, the quotient by 2;
+    # the sum and the products round once each
+    g = np.abs(O.bf16_to_f32(gu)[:, :cols].astype(np.float64))
+    d = (1.173 * g + 8) * 2 * U
+    st = status()
+    if fmt == "e4m3":
+        q, s = sp().fp8_silu_mul_quantize_pertoken(dev_bf16(gu), status=st)
+        check_e4m3(q, s, y, d)
+    else:
+        q, b, s = sp().fp4_silu_mul_quantize_microscaled(dev_bf16(gu), fmt, status=st)
+        check_fp4(q, b, s, y, d, fmt)
+    assert int(st.item()) == 0
+
+
+def test_gate_flags_a_nonfinite_row():
+    gu = WL.random_bits((4, 128), 12)
+    good_q, good_s = sp().fp8_silu_mul_quantize_pertoken(dev_bf16(gu))
+    gu[2, 3], gu[2, 64 + 3] = 0x7F00, 0x7F00                # a product beyond fp32
+    st = status()
+    q, s = sp().fp8_silu_mul_quantize_pertoken(dev_bf16(gu), status=st)
+    assert int(st.item()) == sp()._lib.SP24_STATUS_NONFINITE
+    keep = [0, 1, 3]
+    assert torch.equal(q[keep], good_q[keep]) and torch.equal(s[keep], good_s[keep])
+
+
+# ------------------------------------------------------------------ product
+def operand(rows, k, fmt, seed):
+    """Random codes and block-scale bytes (zeros among them): numpy codes and
+    bytes, and the same on the device as the product takes them."""
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 16, (rows, k)).astype(np.uint8)
+    n = k // MO.BLOCK[fmt]
+    byts = (rng.integers(0x20, 0x58, (rows, n)) if fmt == "nvfp4" else rng.integers(118, 132, (rows, n))).astype(np.uint8)
+    byts[rng.random((rows, n)) < 0.05] = 0
+    return codes, byts, torch.from_numpy(pack(codes)).to(DEV), torch.from_numpy(MO.to_tiles(byts)).to(DEV)
+
+
+def dev_values(codes, byts, fmt):
+    """code * block scale as float64 on the device."""
+    grid = torch.from_numpy(O.e2m1_decode(np.arange(16, dtype=np.uint8))).to(DEV)
+    v = grid[torch.from_numpy(codes.astype(np.int32)).to(DEV).long()]
+    s = torch.from_numpy(MO.scale_values(byts, fmt)).to(DEV)
+    return v * s.repeat_interleave(MO.BLOCK[fmt], 1)
+
+
+def check_product(y, xv, wv, xs, ws):
+    """|y - ref| <= half a bf16 step of ref + what fp32 sums may lose: every
+    product is exact (12 significant bits); the sum of K of them in groups of
+    64 is K / 64 + 64 roundings deep, a rounding taken as a whole fp32 step."""
+    k = xv.shape[1]
+    scale = torch.ones(1, 1, dtype=torch.float64, device=DEV)
+    if xs is not None:
+        scale = scale * xs.double().reshape(-1, 1)
+    if ws is not None:
+        scale = scale * ws.double().reshape(1, -1)
+    ref = xv @ wv.t() * scale
+    mag = xv.abs() @ wv.abs().t() * scale.abs()
+    lost = (k / 64 + 64) * 2 * U * mag + 2 * U * ref.abs()
+    tol = 2.0 ** -8 * (ref.abs() + lost) + lost
+    off = (y.double() - ref).abs()
+    ok = off <= tol
+    assert bool(ok.all()), f"{int((~ok).sum())} of {ok.numel()} outside; first {torch.argwhere(~ok)[:4].tolist()}"
+
+
+PSHAPES = [(1, 8, 64), (1, 128, 256), (2, 136, 192), (3, 4104, 320), (8, 256, 4096), (16, 1000, 1024), (17, 512, 2112),
+           (33, 384, 1024), (64, 2048, 512), (100, 264, 4160), (128, 4096, 448), (129, 520, 832), (256, 1024, 1088),
+           (300, 2304, 2048), (515, 1160, 576), (1000, 520, 4160), (2050, 1032, 704), (1, 11008, 4096), (1, 96, 28672)]
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("m,n,k", PSHAPES)
+def test_product(fmt, m, n, k):
+    xc, xb, xq, xt = operand(m, k, fmt, 7000 + m)
+    wc, wb, wq, wt = operand(n, k, fmt, 8000 + n)
+    g = torch.Generator(device=DEV).manual_seed(m * 7 + n)
+    xs = torch.rand(m, device=DEV, generator=g) + 0.5
+    ws = (torch.rand(n, device=DEV, generator=g) + 0.5) * 0.01
+    st = status()
+    # the result lies inside a larger buffer whose other values must stay
+    buf = torch.full((m * n + 64,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[32:32 + m * n].view(m, n)
+    y = sp().fp4_gemm_microscaled(xq, xt, xs, wq, wt, ws, fmt, out=out, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert bool((buf[:32] == 7).all()) and bool((buf[32 + m * n:] == 7).all())
+    check_product(y, dev_values(xc, xb, fmt), dev_values(wc, wb, fmt), xs, ws)
+    again = sp().fp4_gemm_microscaled(xq, xt, xs, wq, wt, ws, fmt)
+    assert torch.equal(again, y), "the same inputs gave other bits"
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_product_scale_forms(fmt):
+    for m, n, k in ((5, 264, 512), (200, 512, 512)):
+        xc, xb, xq, xt = operand(m, k, fmt, 1)
+        wc, wb, wq, wt = operand(n, k, fmt, 2)
+        xv, wv = dev_values(xc, xb, fmt), dev_values(wc, wb, fmt)
+        vec_m, vec_n = torch.rand(m, device=DEV) + 0.1, torch.rand(n, device=DEV) + 0.1
+        one = torch.tensor([0.37], device=DEV)
+        for xs in (None, one, vec_m):
+            for ws in (None, one, vec_n):
+                check_product(sp().fp4_gemm_microscaled(xq, xt, xs, wq, wt, ws, fmt), xv, wv, xs, ws)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("m,n,k", [(4, 256, 512), (300, 512, 512)])
+def test_product_keeps_a_bad_row_to_itself(fmt, m, n, k):
+    """A NaN scale in one row of either operand reaches that row's (column's) results only."""
+    nan = 0x7F if fmt == "nvfp4" else 0xFF
+    xc, xb, xq, xt = operand(m, k, fmt, 3)
+    wc, wb, wq, wt = operand(n, k, fmt, 4)
+    good = sp().fp4_gemm_microscaled(xq, xt, None, wq, wt, None, fmt)
+    xb2, wb2 = xb.copy(), wb.copy()
+    xb2[2, 1], wb2[100, 0] = nan, nan
+    y = sp().fp4_gemm_microscaled(xq, torch.from_numpy(MO.to_tiles(xb2)).to(DEV), None, wq,
+                                  torch.from_numpy(MO.to_tiles(wb2)).to(DEV), None, fmt)
+    assert bool(y[2].isnan().all()) and bool(y[:, 100].isnan().all())
+    rows = [i for i in range(m) if i != 2]
+    cols = [i for i in range(n) if i != 100]
+    assert torch.equal(y[rows][:, cols], good[rows][:, cols])
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 520, 1024), (300, 520, 1024)])
+def test_product_ignores_scales_outside_the_matrix(m, n, k):
+    """The tiles' unused places may hold anything: only the matrix's rows and
+    blocks are used."""
+    for fmt in ("nvfp4", "mxfp4"):
+        k2 = k + (64 if fmt == "mxfp4" else 0)              # a last tile half used
+        xc, xb, xq, xt = operand(m, k2, fmt, 5)
+        wc, wb, wq, wt = operand(n, k2, fmt, 6)
+        y = sp().fp4_gemm_microscaled(xq, xt, None, wq, wt, None, fmt)
+        for t, rows in ((xt, m), (wt, n)):
+            mask = torch.ones_like(t, dtype=torch.bool)
+            mask[torch.from_numpy(MO.tile_offsets(rows, k2 // MO.BLOCK[fmt])).to(DEV).reshape(-1)] = False
+            t[mask] = 0xFF
+        assert torch.equal(sp().fp4_gemm_microscaled(xq, xt, None, wq, wt, None, fmt), y)
+
+
+def test_long_rows_pass_32_bit_offsets():
+    """A matrix of more than 2^31 elements: its last rows are as when alone."""
+    rows, cols = 66000, 32768
+    x = torch.randn(128, cols, device=DEV).to(torch.bfloat16).repeat(-(-rows // 128), 1)[:rows].contiguous()
+    q, b, s = sp().fp4_quantize_microscaled(x, "nvfp4")
+    lo = (rows // 128) * 128
+    q0, b0, s0 = sp().fp4_quantize_microscaled(x[lo:].contiguous(), "nvfp4")
+    assert torch.equal(q[lo:], q0) and torch.equal(s[lo:], s0)
+    assert torch.equal(b[lo // 128 * (cols // 64) * 512:], b0)
+    del x
+    # and as an operand of a product
+    w = torch.randn(64, cols, device=DEV).to(torch.bfloat16)
+    wq, wb, ws = sp().fp4_quantize_microscaled(w, "nvfp4")
+    y = sp().fp4_gemm_microscaled(q, b, s, wq, wb, ws)
+    y0 = sp().fp4_gemm_microscaled(q0, b0, s0, wq, wb, ws)
+    torch.testing.assert_close(y[lo:].float(), y0.float(), rtol=2.0 ** -7, atol=1e-3)
+
+
+# ------------------------------------------------------------------ use together
+def _ffn_fp4(x, r, w, wgu, wd, fmt, st=None):
+    m = sp()
+    q, b, s, h = m.fp4_rmsnorm_quantize_microscaled(x, w, 1e-5, fmt, residual=r, status=st)
+    gu = m.fp4_gemm_microscaled(q, b, s, *wgu, fmt, status=st)
+    q, b, s = m.fp4_silu_mul_quantize_microscaled(gu, fmt, status=st)
+    return m.fp4_gemm_microscaled(q, b, s, *wd, fmt, status=st), gu, h
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("m", [1, 37, 300])
+def test_feed_forward_block_fp4(fmt, m):
+    """norm -> gate/up product -> gated activation -> down product, each stage
+    held to the oracle on what the stage before it gave."""
+    d, f = 512, 1088
+    x, r = WL.random_bits((m, d), 1), WL.random_bits((m, d), 2)
+    w = WL.random_bits((1, d), 3)[0]
+    gu_w, d_w = WL.random_bits((2 * f, d), 4, scale=0.05), WL.random_bits((d, f), 5, scale=0.05)
+    wgu = sp().fp4_quantize_microscaled(dev_bf16(gu_w), fmt)
+    wd = sp().fp4_quantize_microscaled(dev_bf16(d_w), fmt)
+    st = status()
+    y, gu, h = _ffn_fp4(dev_bf16(x), dev_bf16(r), dev_bf16(w), wgu, wd, fmt, st)
+    assert int(st.item()) == 0
+    yn, hn = MO.rmsnorm(x, r, w, 1e-5)
+    assert np.array_equal(bits_of(h), hn)
+
+    def decoded(q, b, s):
+        rows, cols = q.shape[0], 2 * q.shape[1]
+        v = MO.values(unpack(q), rows_of(b, rows, cols, fmt), fmt)
+        return torch.from_numpy(v).to(DEV), s
+
+    q, b, s, _ = sp().fp4_rmsnorm_quantize_microscaled(dev_bf16(x), dev_bf16(w), 1e-5, fmt, residual=dev_bf16(r))
+    check_fp4(q, b, s, yn, norm_error(d), fmt)
+    (xv, xs), (wv, ws) = decoded(q, b, s), decoded(*wgu)
+    check_product(gu, xv, wv, xs, ws)
+    q, b, s = sp().fp4_silu_mul_quantize_microscaled(gu, fmt)
+    (xv, xs), (wv, ws) = decoded(q, b, s), decoded(*wd)
+    check_product(y, xv, wv, xs, ws)
+
+
+@pytest.mark.parametrize("m", [1, 40, 200])
+def test_feed_forward_block_fp8_sparse(m):
+    """The same run through the 2:4 FP8 product with per-token scales."""
+    d, f = 512, 640
+    x, r = dev_bf16(WL.random_bits((m, d), 1)), dev_bf16(WL.random_bits((m, d), 2))
+    w = dev_bf16(WL.random_bits((1, d), 3)[0])
+    st = status()
+    packed = []
+    for shape, seed in (((2 * f, d), 4), ((d, f), 5)):
+        c = sp().sp24_prune_compress_perchannel(dev_bf16(WL.random_bits(shape, seed, scale=0.05)), status=st)
+        packed.append((sp().sp24_pack_weights(c["values"], c["meta"]), c["scales"], c))
+    q, s, h = sp().fp8_rmsnorm_quantize_pertoken(x, w, 1e-5, residual=r, status=st)
+    gu = sp().sp24_gemm_packed_scaled(q, s, packed[0][0], packed[0][1], 2 * f, status=st)
+    q2, s2 = sp().fp8_silu_mul_quantize_pertoken(gu, status=st)
+    y = sp().sp24_gemm_packed_scaled(q2, s2, packed[1][0], packed[1][1], d, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for out, (qq, ss), (_, wsc, c) in ((gu, (q, s), packed[0]), (y, (q2, s2), packed[1])):
+        dense = O.decompress24(c["values"].cpu().numpy(), c["meta"].cpu().numpy(), qq.shape[1])
+        ref, bound = O.gemm_ref_scaled(O.e4m3_decode(qq.cpu().numpy()), O.e4m3_decode(dense), ss.cpu().numpy(),
+                                       wsc.cpu().numpy())
+        got = O.bf16_to_f32(bits_of(out)).astype(np.float64)
+        assert O.within_tolerance(got, ref, bound).all()
+
+
+@pytest.mark.parametrize("m", [1, 200])
+def test_capture_replay_and_two_graphs_at_once(m):
+    """The block captured twice, replayed on new inputs on two streams at once:
+    the results of eager calls."""
+    fmt, d, f = "nvfp4", 512, 1024
+    w = dev_bf16(WL.random_bits((1, d), 3)[0])
+    wgu = sp().fp4_quantize_microscaled(dev_bf16(WL.random_bits((2 * f, d), 4, scale=0.05)), fmt)
+    wd = sp().fp4_quantize_microscaled(dev_bf16(WL.random_bits((d, f), 5, scale=0.05)), fmt)
+    ins = [dev_bf16(WL.random_bits((m, d), 10 + i)) for i in range(8)]
+    want = [_ffn_fp4(ins[2 * i], ins[2 * i + 1], w, wgu, wd, fmt)[0].clone() for i in range(4)]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        x, r = torch.empty_like(ins[0]), torch.empty_like(ins[0])
+        x.copy_(ins[0])
+        r.copy_(ins[1])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = _ffn_fp4(x, r, w, wgu, wd, fmt)[0]
+        graphs.append((g, x, r, y))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for pair in ((0, 1), (2, 3)):
+        for i, (g, x, r, y), s in zip(pair, graphs, streams):
+            with torch.cuda.stream(s):
+                x.copy_(ins[2 * i])
+                r.copy_(ins[2 * i + 1])
+                for _ in range(3):
+                    g.replay()
+        torch.cuda.synchronize()
+        for i, (g, x, r, y) in zip(pair, graphs):
+            assert torch.equal(y, want[i])
+
+
+def test_calls_on_two_streams_at_once_and_after_foreign_work():
+    """Calls on side streams, each behind the kernel that makes its input."""
+    fmt = "mxfp4"
+    w = torch.randn(1024, 512, device=DEV).to(torch.bfloat16)
+    wq = sp().fp4_quantize_microscaled(w, fmt)
+    xs = [torch.randn(m, 512, device=DEV).to(torch.bfloat16) for m in (1, 70, 260, 1)]
+    want = [sp().fp4_gemm_microscaled(*sp().fp4_quantize_microscaled(2 * x, fmt), *wq, fmt) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        got = []
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                got.append(sp().fp4_gemm_microscaled(*sp().fp4_quantize_microscaled(2 * x, fmt), *wq, fmt))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_python_refusals():
+    m = sp()
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(64, dtype=torch.bfloat16, device=DEV)
+    q, b, s = m.fp4_quantize_microscaled(x)
+    E = m.Sp24Error
+    for bad in (x.float(), x[0], x.t(), x[:, :48].contiguous(), x[:0]):
+        with pytest.raises(E):
+            m.fp4_quantize_microscaled(bad)
+        with pytest.raises(E):
+            m.fp4_rmsnorm_quantize_microscaled(bad, w, 1e-5)
+    with pytest.raises(E):
+        m.fp4_quantize_microscaled(x, "fp4")
+    for bad in (dict(q=q[:2]), dict(block_scales=b[:256]), dict(row_scales=s.double()), dict(q=q.cpu())):
+        with pytest.raises(E):
+            m.fp4_quantize_microscaled(x, out=bad)
+    with pytest.raises(E):
+        m.fp4_quantize_microscaled(x, status=torch.zeros(1, device=DEV))
+    for kw in (dict(weight=w[:32]), dict(weight=w.float()), dict(residual=x[:2]), dict(residual=x.float()),
+               dict(residual_out=x), dict(residual=x, residual_out=x.cpu()), dict(eps=-1.0), dict(eps=float("nan"))):
+        with pytest.raises(E):
+            m.fp8_rmsnorm_quantize_pertoken(x, **{"weight": w, "eps": 1e-5, **kw})
+    with pytest.raises(E):
+        m.fp8_silu_mul_quantize_pertoken(x[:, :33].contiguous())
+    with pytest.raises(E):
+        m.fp4_unpack_e4m3(q.view(torch.int8))
+    for args in ((q, b, s[:2], q, b, s), (q, b[:256], s, q, b, s), (q, b, s, q[:, :16].contiguous(), b, s),
+                 (q, b, s, q, b, s.cpu()), (q, b, s, q[:3], b, s), (q.view(torch.int8), b, s, q, b, s)):
+        with pytest.raises(E):
+            m.fp4_gemm_microscaled(*args)
+    y = torch.zeros(4, 4, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(E):      # N = 4
+        m.fp4_gemm_microscaled(q, b, s, q, b, s, out=y)
+    with pytest.raises(E):      # out is of another type
+        m.fp4_gemm_microscaled(q, b, s, torch.cat([q, q]), b, None, out=torch.zeros(4, 8, device=DEV))
