@@ -463,7 +463,7 @@ int fp4_unpack_e4m3(const uint8_t *q, int64_t rows, int64_t cols, uint8_t *out, 
  * w_scale(n) likewise.  Xq u8 [M, K / 2], Wq u8 [N, K / 2], block scales in
  * the tiles above, of [M, K] and [N, K].  Y bf16 [M, N] must not alias an
  * input.  No workspace; the same inputs give the same bits.  Shape rules:
- * M >= 1, N % 8 == 0, K % 64 == 0, N >= 8, K >= 64.
+ * 1 <= M <= 2^31 - 256, 8 <= N <= 2^31 - 256, N % 8 == 0, K >= 64, K % 64 == 0.
  */
 int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const float *x_scales, int x_per_token,
                          const uint8_t *Wq, const uint8_t *w_block_scales, const float *w_scales, int w_per_channel,

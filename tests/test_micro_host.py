@@ -141,7 +141,7 @@ def test_gemm_refusals(lib):
         assert call(**{a: ODD}) == _lib.SP24_ERR_ALIGN
     for a in ("xs", "ws"):
         assert call(**{a: ODD}) == _lib.SP24_ERR_ALIGN
-    for bad in (dict(m=0), dict(n=0), dict(n=12), dict(n=-8), dict(k=0), dict(k=32), dict(k=96), dict(k=-64)):
+    for bad in (dict(m=0), dict(m=(1 << 31) - 1), dict(n=0), dict(n=(1 << 31) - 8), dict(n=12), dict(n=-8), dict(k=0), dict(k=32), dict(k=96), dict(k=-64)):
         assert call(**bad) == _lib.SP24_ERR_SHAPE
 
 
