@@ -43,6 +43,7 @@ namespace {
 constexpr int kStageK = 256;            // K elements per pipeline stage
 constexpr int kRowBytes = kStageK / 2;  // one swizzled row of codes
 constexpr int kStepK = 64;              // K per MMA
+constexpr int kMaxSlices = 8;           // CTAs that share a narrow tile's K (a portable cluster)
 
 // Instruction descriptor of kinds mxf4 / mxf4nvf4: E2M1 operands (1), both
 // K-major; scale type UE4M3 (0) or UE8M0 (1) at bit 23; N >> 3 at 17, M >> 7
@@ -86,14 +87,15 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+// Bulk copy of this CTA's shared memory into another CTA of the cluster,
+// counted on that CTA's mbarrier (dst and bar: shared::cluster addresses).
+__device__ __forceinline__ void bulk_push(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_addr(src)), "r"(bytes), "r"(bar)
                : "memory");
-  return v;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -113,6 +115,13 @@ struct MicroParams {
 
 // ------------------------------------------------------------------ narrow
 
+// K slices of a tile are joined in shared memory: slice i owns the tile's
+// tokens [i * per, (i + 1) * per); every slice lays its fp32 sums out [token]
+// [128 rows], copies each other owner's tokens into that CTA (one bulk copy
+// each: plain stores into another CTA's shared memory moved about 5 bytes/ns
+// per SM, which made a 128 x 256 tile's join 20 us), and the owner adds them,
+// slices in order.  Up to 32 tokens what arrives has room of its own; wider
+// tiles take it over the ring, once every CTA has finished its main loop.
 template <int BLOCK, int BN>
 struct Narrow {
   static constexpr int kAtoms = kStageK / BLOCK / 4;  // 512-byte scale tiles per band and stage
@@ -121,18 +130,25 @@ struct Narrow {
   static constexpr uint32_t kSfBytes = kAtoms * 512;
   static constexpr uint32_t kBOff = kABytes, kSfaOff = kBOff + kBBytes, kSfbOff = kSfaOff + kSfBytes;
   static constexpr uint32_t kStageBytes = kSfbOff + kSfBytes;
-  // two CTAs on an SM
-  static constexpr int kStages = (112 * 1024 - 2048) / kStageBytes;
-  static constexpr uint32_t kSmem = kStages * kStageBytes + 1024 /*align*/ + 1024 /*barriers*/;
+  static constexpr bool kOwnRoom = BN <= 32;
+  // (slices - 1) * ceil(BN / slices) tokens arrive at most
+  static constexpr uint32_t kPartBytes = (BN + kMaxSlices - 2) * 512;
+  // two CTAs on an SM, but for the widest tile
+  static constexpr int kPerSm = BN <= 64 ? 2 : 1;
+  static constexpr uint32_t kBudget = (kPerSm == 2 ? 112 : 200) * 1024;
+  static constexpr int kStages = (kBudget - 2048 - (kOwnRoom ? kPartBytes : 0)) / kStageBytes;
+  static constexpr uint32_t kPartOff = kOwnRoom ? kStages * kStageBytes : BN * 512;
+  static constexpr uint32_t kBarOff = kStages * kStageBytes + (kOwnRoom ? kPartBytes : 0);
+  static constexpr uint32_t kSmem = kBarOff + 1024 /*align*/ + 1024 /*barriers*/;
   static constexpr uint32_t kSfCols = 8 * kAtoms;  // A's and B's scales of a stage; two stages' worth
   static constexpr uint32_t kTmemNeed = BN + 2 * kSfCols;
   static constexpr uint32_t kTmemCols = kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128 : 256;
   static_assert(kStageBytes % 1024 == 0 && BN % 16 == 0 && BN <= 128, "tile");
-  static_assert(kStages >= 2 && BN * 128 * 4 <= kStages * kStageBytes, "partial sums reuse the ring");
+  static_assert(kStages >= 2 && BN * 512 + (kOwnRoom ? 0 : kPartBytes) <= kStages * kStageBytes, "sums fit the ring");
 };
 
 template <int BLOCK, int BN>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(192, Narrow<BLOCK, BN>::kPerSm)
     narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                   const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
                   const MicroParams p) {
@@ -140,17 +156,21 @@ __global__ void __launch_bounds__(192, 2)
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * C::kStageBytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
   uint64_t *empty = full + S;
   uint64_t *done = empty + S;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  uint64_t *arrived = done + 1;  // the other slices' sums
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(arrived + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slice = static_cast<int>(blockIdx.x) % p.slices, tile = static_cast<int>(blockIdx.x) / p.slices;
   const int n0 = (tile % p.tiles_n) * 128, m0 = (tile / p.tiles_n) * BN;
-  // this slice's stages
+  // this slice's stages, and its tokens of the tile
   const int s0 = static_cast<int>(static_cast<int64_t>(slice) * p.stages / p.slices);
   const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * p.stages / p.slices);
+  const int mvalid = min(BN, p.M - m0);
+  const int per = (mvalid + p.slices - 1) / p.slices;
+  const int c0 = min(mvalid, slice * per), c1 = min(mvalid, c0 + per);
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmW);
@@ -162,7 +182,9 @@ __global__ void __launch_bounds__(192, 2)
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
+    mbar_init(arrived, 1);
     fence_mbar_init();
+    mbar_arrive_expect_tx(arrived, (p.slices - 1) * (c1 - c0) * 512);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kTmemCols);
@@ -171,6 +193,7 @@ __global__ void __launch_bounds__(192, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.slices > 1) cluster_arrive();  // this CTA runs and its barriers exist
   const uint32_t tmem = *tmem_slot;
   // Everything the kernel reads may come from the kernel before it.
   grid_dependency_wait();
@@ -225,66 +248,74 @@ __global__ void __launch_bounds__(192, 2)
     }
     if (leader) mma_commit(done);
     __syncwarp();
-  } else {
-    const int q = warp & 3, row = q * 32 + lane, n = n0 + row;
-    const int mvalid = min(BN, p.M - m0);
-    const float w1 = p.ws && !p.w_vec ? __ldg(p.ws) : 1.0f, x1 = p.xs && !p.x_vec ? __ldg(p.xs) : 1.0f;
-    const float wsn = p.w_vec && n < p.N ? __ldg(p.ws + n) : w1;
+  }
+
+  // ---- epilogue: warps 2-5 hold 32 weight rows each (their lanes)
+  const int q = warp & 3, row = q * 32 + lane, n = n0 + row;
+  float wsn = 1.0f, x1 = 1.0f;
+  if (warp >= 2) {
+    if (p.ws) wsn = __ldg(p.ws + (p.w_vec ? min(n, p.N - 1) : 0));
+    if (p.xs && !p.x_vec) x1 = __ldg(p.xs);
     mbar_wait(done, 0u, p.status);
     tc_fence_after();
+  }
+  auto store = [&](int m, float sum) {
+    const float xsm = p.x_vec ? __ldg(p.xs + m) : x1;
+    p.y[static_cast<int64_t>(m) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum * (xsm * wsn)));
+  };
+  if (p.slices > 1) {
+    __syncwarp();
+    cluster_wait();
+    if (!C::kOwnRoom) {
+      cluster_arrive();
+      cluster_wait();
+    }
+  }
+  if (warp >= 2) {
     const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    float *part = reinterpret_cast<float *>(smem);
+    float *sums = reinterpret_cast<float *>(smem) + row;
 #pragma unroll 1
     for (int c = 0; c < mvalid; c += 16) {
       uint32_t v[16];
       tmem_ld_32x32b_x16(t_row + c, v);
       tmem_ld_wait();
       tmem_regs_ready(v);
-      if (p.slices > 1) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) part[(c + k) * 128 + row] = __uint_as_float(v[k]);
-      } else if (n < p.N) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int m = m0 + c + k;
-          if (c + k < mvalid) {
-            const float xsm = p.x_vec ? __ldg(p.xs + m) : x1;
-            p.y[static_cast<int64_t>(m) * p.N + n] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[k]) * (xsm * wsn)));
-          }
+      for (int k = 0; k < 16; ++k) {
+        if (p.slices > 1) {
+          sums[(c + k) * 128] = __uint_as_float(v[k]);
+        } else if (c + k < mvalid && n < p.N) {
+          store(m0 + c + k, __uint_as_float(v[k]));
         }
       }
     }
     tc_fence_before();
-  }
-  if (p.slices > 1) {
-    __syncwarp();
-    cluster_sync_all();
-    if (warp >= 2) {
-      const int mvalid = min(BN, p.M - m0);
-      const float w1 = p.ws && !p.w_vec ? __ldg(p.ws) : 1.0f, x1 = p.xs && !p.x_vec ? __ldg(p.xs) : 1.0f;
-      const int step = 128 * p.slices;
-      for (int e = static_cast<int>(threadIdx.x) - 64 + 128 * slice; e < mvalid * 32; e += step) {
-        const int m = m0 + e / 32, n = n0 + (e % 32) * 4;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int r = 0; r < p.slices; ++r) {  // in slice order: the same sum every time
-          const float4 v = ld_cluster_f4(mapa_shared(smem + e * 16, r));
-          sum.x += v.x;
-          sum.y += v.y;
-          sum.z += v.z;
-          sum.w += v.w;
-        }
-        if (n < p.N) {
-          const float xsm = p.x_vec ? __ldg(p.xs + m) : x1;
-          const float4 w = p.w_vec ? __ldg(reinterpret_cast<const float4 *>(p.ws + n)) : make_float4(w1, w1, w1, w1);
-          *reinterpret_cast<uint2 *>(p.y + static_cast<int64_t>(m) * p.N + n) =
-              make_uint2(pack_bf16(sum.x * (xsm * w.x), sum.y * (xsm * w.y)),
-                         pack_bf16(sum.z * (xsm * w.z), sum.w * (xsm * w.w)));
+    if (p.slices > 1) {
+      fence_proxy_async_smem();
+      named_bar_sync(1, 128);
+      if (warp == 2 && lane < p.slices && lane != slice) {
+        const int o0 = min(mvalid, lane * per), o1 = min(mvalid, o0 + per), from = slice - (slice > lane ? 1 : 0);
+        if (o1 > o0)
+          bulk_push(mapa_shared(smem + C::kPartOff + from * per * 512, lane), smem + o0 * 512, (o1 - o0) * 512,
+                    mapa_shared(arrived, lane));
+      }
+      __syncwarp();
+      mbar_wait_cluster(arrived, 0u, p.status);
+      const float *part = reinterpret_cast<const float *>(smem + C::kPartOff) + row;
+      if (n < p.N) {
+        for (int c = c0; c < c1; ++c) {
+          float sum = sums[c * 128];
+#pragma unroll
+          for (int r = 0; r < kMaxSlices - 1; ++r)
+            if (r < p.slices - 1) sum += part[(r * per + c - c0) * 128];
+          store(m0 + c, sum);
         }
       }
     }
+  }
+  if (p.slices > 1) {
     __syncwarp();
-    cluster_sync_all();  // nobody leaves while its partial sums are read
+    cluster_sync_all();  // nobody leaves while its sums are being copied
   }
   tc_fence_before();
   __syncthreads();
@@ -302,7 +333,8 @@ __global__ void __launch_bounds__(192, 2)
 // columns that overlap in 64 (0..255 and 192..447), and 64 columns of scales.
 // A tile's epilogue first takes the 64 shared columns to registers and gives
 // them free; the next tile's main loop, in the other accumulator, then runs
-// beside the rest of the epilogue.
+// beside the rest of the epilogue.  Y leaves through shared memory, 32 tokens
+// x 64 columns per bulk tensor store.
 template <int BLOCK>
 struct Wide {
   static constexpr int kAtoms = kStageK / BLOCK / 4;
@@ -312,12 +344,17 @@ struct Wide {
   static constexpr uint32_t kStageBytes = kSfbOff + 2 * kSfBytes;
   static constexpr uint32_t kStagePitch = (kStageBytes + 1023) / 1024 * 1024;
   static constexpr int kStages = 5;
-  static constexpr uint32_t kPartPitch = 260;  // floats per token row of a partial tile
-  static constexpr uint32_t kSmem = kStages * kStagePitch + 2048;
+  static constexpr uint32_t kYBytes = 32 * 128;             // one warp's staged 32 x 64 of Y
+  static constexpr uint32_t kYOff = kStages * kStagePitch;  // two per epilogue warp
+  static constexpr uint32_t kWsOff = kYOff + 8 * kYBytes;   // weight scales of two tiles
+  static constexpr uint32_t kBarOff = kWsOff + 2 * 256 * 4;
+  static constexpr uint32_t kSmem = kBarOff + 1024 + 1024 /*align*/;
   static constexpr uint32_t kSfCols = 12 * kAtoms;                 // A 4, B 8 per 512-byte tile of A
   static constexpr uint32_t kSfSlots = kSfCols * 2 <= 64 ? 2 : 1;  // stages' scales held at once
   static_assert(kSfCols * kSfSlots <= 64, "scale columns");
-  static_assert(128 * kPartPitch * 4 <= kStages * kStagePitch, "partial sums reuse the ring");
+  // K slices: three quarters of a 128 x 256 tile leave and as many arrive
+  static constexpr uint32_t kPartOff = 3 * 128 * 64 * 4;
+  static_assert(2 * kPartOff <= kWsOff, "partial sums reuse the ring and the staged Y");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -325,16 +362,17 @@ template <int BLOCK>
 __global__ void __launch_bounds__(192, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
-                const MicroParams p) {
+                const __grid_constant__ CUtensorMap tmY, const MicroParams p) {
   using C = Wide<BLOCK>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * C::kStagePitch);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
   uint64_t *empty = full + S;
-  uint64_t *acc_full = empty + S;      // [2]: accumulator complete
+  uint64_t *acc_full = empty + S;        // [2]: accumulator complete
   uint64_t *shared_free = acc_full + 2;  // a tile's shared columns are in registers
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(shared_free + 1);
+  uint64_t *arrived = shared_free + 1;   // the other slices' sums
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(arrived + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
@@ -350,6 +388,7 @@ __global__ void __launch_bounds__(192, 1)
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmSW);
     prefetch_tensormap(&tmSX);
+    prefetch_tensormap(&tmY);
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -357,7 +396,9 @@ __global__ void __launch_bounds__(192, 1)
     mbar_init(&acc_full[0], 1);
     mbar_init(&acc_full[1], 1);
     mbar_init(shared_free, 256);  // both CTAs' epilogue threads
+    mbar_init(arrived, 1);
     fence_mbar_init();
+    mbar_arrive_expect_tx(arrived, (p.slices - 1) * (64 / p.slices) * 2048);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -452,20 +493,27 @@ __global__ void __launch_bounds__(192, 1)
       }
     }
     __syncwarp();
-  } else {
-    const int q = warp & 3, row = q * 32 + lane;
-    const float w1 = p.ws && !p.w_vec ? __ldg(p.ws) : 1.0f, x1 = p.xs && !p.x_vec ? __ldg(p.xs) : 1.0f;
+  } else if (p.slices == 1) {
+    const int e = warp - 2, q = warp & 3;
+    float *wsm = reinterpret_cast<float *>(smem + C::kWsOff);
     int j = 0;
+    uint32_t pass = 0;
     for (int t = first; t < tiles; t += step, ++j) {
-      const int m = (t % p.tiles_m) * 256 + static_cast<int>(rank) * 128 + row, n0 = (t / p.tiles_m) * 256;
-      const float xsm = p.x_vec && m < p.M ? __ldg(p.xs + m) : x1;
-      if (!mbar_wait(&acc_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, p.status)) break;
+      const int mq = (t % p.tiles_m) * 256 + static_cast<int>(rank) * 128 + q * 32, n0 = (t / p.tiles_m) * 256;
+      float xsm = 1.0f;
+      if (p.xs) xsm = __ldg(p.xs + (p.x_vec ? min(mq + lane, p.M - 1) : 0));
+      // the tile's weight scales, in the buffer of the tile before last
+      float *wt = wsm + (j & 1) * 256;
+      for (int k = static_cast<int>(threadIdx.x) - 64; k < 256; k += 128)
+        wt[k] = p.ws ? __ldg(p.ws + (p.w_vec ? min(n0 + k, p.N - 1) : 0)) : 1.0f;
+      named_bar_sync(1, 128);
+      mbar_wait(&acc_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, p.status);
       tc_fence_after();
       const uint32_t t_row = tmem + (j & 1) * 192 + (static_cast<uint32_t>(q * 32) << 16);
       // 64 columns at a time, the shared ones first: the last of the lower
       // accumulator, the first of the upper
 #pragma unroll 1
-      for (int h = 0; h < 4; ++h) {
+      for (int h = 0; h < 4; ++h, ++pass) {
         const int c = ((j & 1) ? h : (h + 3) & 3) * 64;
         uint32_t v[64];
         tmem_ld_32x32b_x64(t_row + c, v);
@@ -478,71 +526,112 @@ __global__ void __launch_bounds__(192, 1)
           else
             mbar_arrive_cluster(mapa_shared(shared_free, lead));
         }
-        if (p.slices > 1) {
-          float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(smem) + row * C::kPartPitch + c);
+        uint8_t *buf = smem + C::kYOff + (2 * e + (pass & 1)) * C::kYBytes;
+        if (lane == 0) bulk_wait_group_read<1>();  // the store two passes ago has read it
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            dst[k] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
-                                 __uint_as_float(v[4 * k + 3]));
-        } else if (m < p.M) {
-          uint16_t *y = p.y + static_cast<int64_t>(m) * p.N + n0 + c;
+        for (int k = 0; k < 64; k += 8) {
+          const float4 a = *reinterpret_cast<const float4 *>(wt + c + k), b = *reinterpret_cast<const float4 *>(wt + c + k + 4);
+          const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 64; k += 8) {
-            if (n0 + c + k < p.N) {
-              float f[8];
-              if (p.w_vec) {
-                const float4 a = __ldg(reinterpret_cast<const float4 *>(p.ws + n0 + c + k));
-                const float4 b = __ldg(reinterpret_cast<const float4 *>(p.ws + n0 + c + k + 4));
-                f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-              } else {
-#pragma unroll
-                for (int l = 0; l < 8; ++l) f[l] = w1;
-              }
-#pragma unroll
-              for (int l = 0; l < 8; ++l) f[l] = __uint_as_float(v[k + l]) * (xsm * f[l]);
-              *reinterpret_cast<uint4 *>(y + k) =
-                  make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-            }
-          }
+          for (int l = 0; l < 4; ++l)
+            o[l] = pack_bf16(__uint_as_float(v[k + 2 * l]) * (xsm * f[2 * l]),
+                             __uint_as_float(v[k + 2 * l + 1]) * (xsm * f[2 * l + 1]));
+          // row `lane` of the 128-byte swizzled box: 16-byte chunk i at i ^ (lane & 7)
+          *reinterpret_cast<uint4 *>(buf + lane * 128 + ((k / 8) ^ (lane & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (mq < p.M && n0 + c < p.N) tma_store_2d(&tmY, buf, n0 + c, mq);
+          bulk_commit_group();
         }
       }
     }
     tc_fence_before();
+    if (lane == 0) bulk_wait_group_all();
   }
   __syncwarp();
   if (p.slices > 1) {
-    cluster_sync_all();  // every slice's partial tile is written
+    // One tile per cluster.  Slice i owns 256 / slices columns of the tile;
+    // every slice lays the others' columns out [owner][4 columns][token] over
+    // its ring, copies them to their owners, and adds what arrives to its own,
+    // the other slices in order.
+    const int q = warp & 3, row = q * 32 + lane;
+    const int m = (first % p.tiles_m) * 256 + static_cast<int>(rank) * 128 + row, n0 = (first / p.tiles_m) * 256;
+    const int quads = 64 / p.slices;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
     if (warp >= 2) {
-      // this CTA's columns of its own 128 tokens, over all slices
-      const float w1 = p.ws && !p.w_vec ? __ldg(p.ws) : 1.0f, x1 = p.xs && !p.x_vec ? __ldg(p.xs) : 1.0f;
-      const int m0 = (first % p.tiles_m) * 256 + static_cast<int>(rank) * 128, n0 = (first / p.tiles_m) * 256;
-      const int quads = 64 / p.slices, c0 = quads * slice;  // of 4 columns
-      const int rows = min(128, p.M - m0);
-      for (int e = static_cast<int>(threadIdx.x) - 64; e < rows * quads; e += 128) {
-        const int r = e / quads, c = (c0 + e % quads) * 4, m = m0 + r, n = n0 + c;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k = 0; k < p.slices; ++k) {
-          const float4 v = ld_cluster_f4(mapa_shared(reinterpret_cast<float *>(smem) + r * C::kPartPitch + c, 2 * k + rank));
-          sum.x += v.x;
-          sum.y += v.y;
-          sum.z += v.z;
-          sum.w += v.w;
+      mbar_wait(&acc_full[0], 0u, p.status);
+      tc_fence_after();
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA's ring is in use any more
+    if (warp >= 2) {
+#pragma unroll 1
+      for (int o = 0; o < p.slices; ++o) {
+        if (o == slice) continue;
+        uint8_t *mine = smem + (o - (o > slice ? 1 : 0)) * quads * 2048;
+#pragma unroll 1
+        for (int k = 0; k < quads; k += 8) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(t_row + (o * quads + k) * 4, v);
+          tmem_ld_wait();
+          tmem_regs_ready(v);
+#pragma unroll
+          for (int l = 0; l < 8; ++l)
+            *reinterpret_cast<uint4 *>(mine + ((k + l) * 128 + row) * 16) =
+                make_uint4(v[4 * l], v[4 * l + 1], v[4 * l + 2], v[4 * l + 3]);
         }
-        if (n < p.N) {
-          const float xsm = p.x_vec ? __ldg(p.xs + m) : x1;
-          const float4 w = p.w_vec ? __ldg(reinterpret_cast<const float4 *>(p.ws + n)) : make_float4(w1, w1, w1, w1);
-          *reinterpret_cast<uint2 *>(p.y + static_cast<int64_t>(m) * p.N + n) =
-              make_uint2(pack_bf16(sum.x * (xsm * w.x), sum.y * (xsm * w.y)),
-                         pack_bf16(sum.z * (xsm * w.z), sum.w * (xsm * w.w)));
+        fence_proxy_async_smem();
+        named_bar_sync(1, 128);
+        if (threadIdx.x == 64) {
+          const uint32_t to = static_cast<uint32_t>(2 * o) + rank, from = slice - (slice > o ? 1 : 0);
+          bulk_push(mapa_shared(smem + C::kPartOff + from * quads * 2048, to), mine, quads * 2048, mapa_shared(arrived, to));
+        }
+        __syncwarp();
+      }
+      const float xsm = p.xs ? __ldg(p.xs + (p.x_vec ? min(m, p.M - 1) : 0)) : 1.0f;
+      const float w1 = p.ws && !p.w_vec ? __ldg(p.ws) : 1.0f;
+      mbar_wait_cluster(arrived, 0u, p.status);
+      const float4 *part = reinterpret_cast<const float4 *>(smem + C::kPartOff) + row;
+#pragma unroll 1
+      for (int k = 0; k < quads; k += 8) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(t_row + (slice * quads + k) * 4, v);
+        tmem_ld_wait();
+        tmem_regs_ready(v);
+#pragma unroll
+        for (int l = 0; l < 8; l += 2) {
+          const int n = n0 + (slice * quads + k + l) * 4;
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[4 * l + i]);
+#pragma unroll
+          for (int r = 0; r < 3; ++r) {
+            if (r < p.slices - 1) {
+              const float4 a = part[(r * quads + k + l) * 128], b = part[(r * quads + k + l + 1) * 128];
+              f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w, f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
+            }
+          }
+          if (n < p.N && m < p.M) {
+            float4 a = make_float4(w1, w1, w1, w1), b = a;
+            if (p.w_vec) a = __ldg(reinterpret_cast<const float4 *>(p.ws + n)), b = __ldg(reinterpret_cast<const float4 *>(p.ws + n + 4));
+            *reinterpret_cast<uint4 *>(p.y + static_cast<int64_t>(m) * p.N + n) = make_uint4(
+                pack_bf16(f[0] * (xsm * a.x), f[1] * (xsm * a.y)), pack_bf16(f[2] * (xsm * a.z), f[3] * (xsm * a.w)),
+                pack_bf16(f[4] * (xsm * b.x), f[5] * (xsm * b.y)), pack_bf16(f[6] * (xsm * b.z), f[7] * (xsm * b.w)));
+          }
         }
       }
+      tc_fence_before();
     }
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  // no CTA frees tensor memory or leaves while another may still use it, read
-  // its partial sums or arrive on its barriers
+  // no CTA frees tensor memory or leaves while another may still use it or
+  // arrive on its barriers
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
@@ -583,9 +672,8 @@ int wide_clusters(int size) {
   return cap[size == 2 ? 0 : size == 4 ? 1 : 2];
 }
 
-template <typename Kernel>
-cudaError_t launch(Kernel kernel, unsigned grid, unsigned cluster, uint32_t smem, const CUtensorMap (&tm)[4],
-                   const MicroParams &p, cudaStream_t st) {
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), unsigned grid, unsigned cluster, uint32_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(192, 1, 1);
@@ -599,7 +687,7 @@ cudaError_t launch(Kernel kernel, unsigned grid, unsigned cluster, uint32_t smem
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tm[0], tm[1], tm[2], tm[3], p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Codes [rows, K / 2] as bytes in boxes of 128 bytes x `box` rows; block
@@ -624,17 +712,19 @@ cudaError_t launch_narrow(const MicroGemmArgs &a, MicroParams p, cudaStream_t st
   if (err != cudaSuccess) return err;
   p.tiles_n = (a.N + 127) / 128;
   p.tiles_m = (a.M + BN - 1) / BN;
-  // K slices: as many as leave every CTA resident at once, two on an SM
+  // K slices: as many as leave every CTA resident at once (one
+  // token tile at most 128 wide, so a tile starts at a band of 128 rows)
   const int64_t tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_m;
-  int64_t s = 2 * 148 / tiles;
-  s = s < 1 ? 1 : s > 8 ? 8 : s;
+  int64_t s = C::kPerSm * 148 / tiles;
+  s = s < 1 ? 1 : s > kMaxSlices ? kMaxSlices : s;
   if (s > p.stages) s = p.stages;
   p.slices = static_cast<int>(s);
   CUtensorMap tm[4];
   if (!make_maps(&tm[0], &tm[2], a.wq, a.wb, a.N, a.K, BLOCK, 128) ||
       !make_maps(&tm[1], &tm[3], a.xq, a.xb, a.M, a.K, BLOCK, BN))
     return cudaErrorInvalidValue;
-  return launch(narrow_kernel<BLOCK, BN>, static_cast<unsigned>(tiles * s), static_cast<unsigned>(s), C::kSmem, tm, p, st);
+  return launch(narrow_kernel<BLOCK, BN>, static_cast<unsigned>(tiles * s), static_cast<unsigned>(s), C::kSmem, st, tm[0], tm[1],
+                tm[2], tm[3], p);
 }
 
 template <int BLOCK>
@@ -650,12 +740,13 @@ cudaError_t launch_wide(const MicroGemmArgs &a, MicroParams p, cudaStream_t st) 
   while (s < 4 && tiles * 2 * s <= pairs && 2 * s <= p.stages && wide_clusters<BLOCK>(4 * s) >= 1) s *= 2;
   p.slices = s;
   const int64_t clusters = s > 1 ? tiles : (tiles < pairs ? tiles : pairs);
-  CUtensorMap tm[4];
+  CUtensorMap tm[5];
   if (!make_maps(&tm[0], &tm[2], a.wq, a.wb, a.N, a.K, BLOCK, 128) ||
-      !make_maps(&tm[1], &tm[3], a.xq, a.xb, a.M, a.K, BLOCK, 128))
+      !make_maps(&tm[1], &tm[3], a.xq, a.xb, a.M, a.K, BLOCK, 128) ||
+      !make_tensor_map_2d(&tm[4], a.y, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.N, a.M, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   return launch(wide_kernel<BLOCK>, static_cast<unsigned>(clusters * 2 * s), static_cast<unsigned>(2 * s), Wide<BLOCK>::kSmem,
-                tm, p, st);
+                st, tm[0], tm[1], tm[2], tm[3], tm[4], p);
 }
 
 template <int BLOCK>
