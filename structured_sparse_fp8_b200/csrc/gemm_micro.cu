@@ -44,6 +44,7 @@ constexpr int kStageK = 256;            // K elements per pipeline stage
 constexpr int kRowBytes = kStageK / 2;  // one swizzled row of codes
 constexpr int kStepK = 64;              // K per MMA
 constexpr int kMaxSlices = 8;           // CTAs that share a narrow tile's K (a portable cluster)
+constexpr int kMaxWideSlices = 4;       // SM pairs that share a wide tile's K
 
 // Instruction descriptor of kinds mxf4 / mxf4nvf4: E2M1 operands (1), both
 // K-major; scale type UE4M3 (0) or UE8M0 (1) at bit 23; N >> 3 at 17, M >> 7
@@ -94,8 +95,21 @@ __device__ __forceinline__ void bulk_push(uint32_t dst, const void *src, uint32_
                "r"(smem_addr(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+
+// The CTAs of a cluster order only each other's asynchronous operations here
+// (tensor-memory reads that have returned, bulk copies counted on mbarriers,
+// mbarriers whose initialisation is fenced), never plain stores, so their
+// arrivals are relaxed: a release at cluster scope first waits for the
+// thread's earlier stores, which took 0.6 to 0.7 us of every tile of Y.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_meet() {
+  cluster_arrive();
+  cluster_wait();
+}
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -122,6 +136,17 @@ struct MicroParams {
 // per SM, which made a 128 x 256 tile's join 20 us), and the owner adds them,
 // slices in order.  Up to 32 tokens what arrives has room of its own; wider
 // tiles take it over the ring, once every CTA has finished its main loop.
+
+// Tokens that arrive from other slices at most: (slices - 1) * ceil(BN / slices).
+constexpr uint32_t most_tokens(int bn) {
+  uint32_t most = 0;
+  for (int s = 2; s <= kMaxSlices; ++s) {
+    const uint32_t t = (s - 1) * ((bn + s - 1) / s);
+    most = t > most ? t : most;
+  }
+  return most;
+}
+
 template <int BLOCK, int BN>
 struct Narrow {
   static constexpr int kAtoms = kStageK / BLOCK / 4;  // 512-byte scale tiles per band and stage
@@ -131,15 +156,17 @@ struct Narrow {
   static constexpr uint32_t kBOff = kABytes, kSfaOff = kBOff + kBBytes, kSfbOff = kSfaOff + kSfBytes;
   static constexpr uint32_t kStageBytes = kSfbOff + kSfBytes;
   static constexpr bool kOwnRoom = BN <= 32;
-  // (slices - 1) * ceil(BN / slices) tokens arrive at most
-  static constexpr uint32_t kPartBytes = (BN + kMaxSlices - 2) * 512;
-  // two CTAs on an SM, but for the widest tile
-  static constexpr int kPerSm = BN <= 64 ? 2 : 1;
-  static constexpr uint32_t kBudget = (kPerSm == 2 ? 112 : 200) * 1024;
-  static constexpr int kStages = (kBudget - 2048 - (kOwnRoom ? kPartBytes : 0)) / kStageBytes;
+  static constexpr uint32_t kPartBytes = most_tokens(BN) * 512;
+  // CTAs that share an SM.  The smallest tiles leave room for the next call's
+  // CTAs, whose start (barriers, tensor memory, descriptors: about 1 us) then
+  // hides behind this call.
+  static constexpr int kPerSm = BN <= 16 ? 4 : BN <= 32 ? 3 : BN <= 64 ? 2 : 1;
+  static constexpr uint32_t kBudget = kPerSm == 4 ? 57344 : kPerSm == 3 ? 75776 : kPerSm == 2 ? 114688 : 204800;
+  static constexpr int kStages = (kBudget - 3072 - (kOwnRoom ? kPartBytes : 0)) / kStageBytes;
   static constexpr uint32_t kPartOff = kOwnRoom ? kStages * kStageBytes : BN * 512;
   static constexpr uint32_t kBarOff = kStages * kStageBytes + (kOwnRoom ? kPartBytes : 0);
-  static constexpr uint32_t kSmem = kBarOff + 1024 /*align*/ + 1024 /*barriers*/;
+  static constexpr uint32_t kScaleOff = kBarOff + 512;  // the tile's token scales
+  static constexpr uint32_t kSmem = kScaleOff + 512 + 1024 /*align*/;
   static constexpr uint32_t kSfCols = 8 * kAtoms;  // A's and B's scales of a stage; two stages' worth
   static constexpr uint32_t kTmemNeed = BN + 2 * kSfCols;
   static constexpr uint32_t kTmemCols = kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128 : 256;
@@ -250,30 +277,24 @@ __global__ void __launch_bounds__(192, Narrow<BLOCK, BN>::kPerSm)
     __syncwarp();
   }
 
-  // ---- epilogue: warps 2-5 hold 32 weight rows each (their lanes)
-  const int q = warp & 3, row = q * 32 + lane, n = n0 + row;
-  float wsn = 1.0f, x1 = 1.0f;
+  // ---- epilogue: warps 2-5 hold 32 weight rows each (their lanes), and lay
+  // the sums out [token][128 rows]; then a warp writes one token's 128 results
+  const int q = warp & 3, tid = static_cast<int>(threadIdx.x) - 64;
+  const int n = n0 + 4 * lane;  // of the four results a lane writes
+  float *xsm = reinterpret_cast<float *>(smem + C::kScaleOff);
+  float4 wsn = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
   if (warp >= 2) {
-    if (p.ws) wsn = __ldg(p.ws + (p.w_vec ? min(n, p.N - 1) : 0));
-    if (p.xs && !p.x_vec) x1 = __ldg(p.xs);
+    // the scales, fetched while the main loop runs
+    if (p.ws && p.w_vec) {
+      if (n < p.N) wsn = __ldg(reinterpret_cast<const float4 *>(p.ws + n));
+    } else if (p.ws) {
+      wsn.x = wsn.y = wsn.z = wsn.w = __ldg(p.ws);
+    }
+    for (int c = tid; c < mvalid; c += 128) xsm[c] = p.xs ? __ldg(p.xs + (p.x_vec ? m0 + c : 0)) : 1.0f;
     mbar_wait(done, 0u, p.status);
     tc_fence_after();
-  }
-  auto store = [&](int m, float sum) {
-    const float xsm = p.x_vec ? __ldg(p.xs + m) : x1;
-    p.y[static_cast<int64_t>(m) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum * (xsm * wsn)));
-  };
-  if (p.slices > 1) {
-    __syncwarp();
-    cluster_wait();
-    if (!C::kOwnRoom) {
-      cluster_arrive();
-      cluster_wait();
-    }
-  }
-  if (warp >= 2) {
     const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    float *sums = reinterpret_cast<float *>(smem) + row;
+    float *sums = reinterpret_cast<float *>(smem) + q * 32 + lane;
 #pragma unroll 1
     for (int c = 0; c < mvalid; c += 16) {
       uint32_t v[16];
@@ -281,18 +302,19 @@ __global__ void __launch_bounds__(192, Narrow<BLOCK, BN>::kPerSm)
       tmem_ld_wait();
       tmem_regs_ready(v);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        if (p.slices > 1) {
-          sums[(c + k) * 128] = __uint_as_float(v[k]);
-        } else if (c + k < mvalid && n < p.N) {
-          store(m0 + c + k, __uint_as_float(v[k]));
-        }
-      }
+      for (int k = 0; k < 16; ++k) sums[(c + k) * 128] = __uint_as_float(v[k]);
     }
     tc_fence_before();
+    fence_proxy_async_smem();
+    named_bar_sync(1, 128);
+  }
+  if (p.slices > 1) {
+    __syncwarp();
+    cluster_wait();
+    if (!C::kOwnRoom) cluster_meet();
+  }
+  if (warp >= 2) {
     if (p.slices > 1) {
-      fence_proxy_async_smem();
-      named_bar_sync(1, 128);
       if (warp == 2 && lane < p.slices && lane != slice) {
         const int o0 = min(mvalid, lane * per), o1 = min(mvalid, o0 + per), from = slice - (slice > lane ? 1 : 0);
         if (o1 > o0)
@@ -300,22 +322,30 @@ __global__ void __launch_bounds__(192, Narrow<BLOCK, BN>::kPerSm)
                     mapa_shared(arrived, lane));
       }
       __syncwarp();
-      mbar_wait_cluster(arrived, 0u, p.status);
-      const float *part = reinterpret_cast<const float *>(smem + C::kPartOff) + row;
-      if (n < p.N) {
-        for (int c = c0; c < c1; ++c) {
-          float sum = sums[c * 128];
+      mbar_wait(arrived, 0u, p.status);
+    }
+    const float4 *sums = reinterpret_cast<const float4 *>(smem) + lane;
+    const float4 *part = reinterpret_cast<const float4 *>(smem + C::kPartOff) + lane;
+    if (n < p.N) {
+#pragma unroll 2
+      for (int c = c0 + warp - 2; c < c1; c += 4) {
+        float4 sum = sums[c * 32];
 #pragma unroll
-          for (int r = 0; r < kMaxSlices - 1; ++r)
-            if (r < p.slices - 1) sum += part[(r * per + c - c0) * 128];
-          store(m0 + c, sum);
+        for (int r = 0; r < kMaxSlices - 1; ++r) {
+          if (r < p.slices - 1) {
+            const float4 v = part[(r * per + c - c0) * 32];
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+          }
         }
+        const float x = xsm[c];
+        *reinterpret_cast<uint2 *>(p.y + static_cast<int64_t>(m0 + c) * p.N + n) =
+            make_uint2(pack_bf16(sum.x * (x * wsn.x), sum.y * (x * wsn.y)), pack_bf16(sum.z * (x * wsn.z), sum.w * (x * wsn.w)));
       }
     }
   }
   if (p.slices > 1) {
     __syncwarp();
-    cluster_sync_all();  // nobody leaves while its sums are being copied
+    cluster_meet();  // nobody leaves while its sums are being copied
   }
   tc_fence_before();
   __syncthreads();
@@ -330,11 +360,14 @@ __global__ void __launch_bounds__(192, Narrow<BLOCK, BN>::kPerSm)
 // 256 tokens (A, 128 per CTA) x 256 weight rows (B, 128 per CTA's half); each
 // CTA's accumulator is 128 lanes (its tokens) x 256 columns.  Both CTAs hold
 // the scales of all 256 weight rows.  Tensor memory: two accumulators of 256
-// columns that overlap in 64 (0..255 and 192..447), and 64 columns of scales.
-// A tile's epilogue first takes the 64 shared columns to registers and gives
-// them free; the next tile's main loop, in the other accumulator, then runs
-// beside the rest of the epilogue.  Y leaves through shared memory, 32 tokens
-// x 64 columns per bulk tensor store.
+// columns that share 96 (0..255 and 160..415), and two stages' scales.  Four
+// epilogue warps take the shared columns of a finished tile to registers and
+// give them free at once, and the next tile's main loop, in the other
+// accumulator, runs beside the rest of the epilogue.  Reading tensor memory
+// is slow enough (an accumulator's 128 KB takes 1.2 us) that the other four
+// warps, who hold the accumulator's other half, wait until the shared columns
+// are read.  Y leaves through shared memory, 32 tokens x 32 columns per bulk
+// tensor store.
 template <int BLOCK>
 struct Wide {
   static constexpr int kAtoms = kStageK / BLOCK / 4;
@@ -344,22 +377,26 @@ struct Wide {
   static constexpr uint32_t kStageBytes = kSfbOff + 2 * kSfBytes;
   static constexpr uint32_t kStagePitch = (kStageBytes + 1023) / 1024 * 1024;
   static constexpr int kStages = 5;
-  static constexpr uint32_t kYBytes = 32 * 128;             // one warp's staged 32 x 64 of Y
-  static constexpr uint32_t kYOff = kStages * kStagePitch;  // two per epilogue warp
+  static constexpr int kThreads = 64 + 256;
+  static constexpr uint32_t kAcc1 = 160;                    // first column of the second accumulator
+  static constexpr uint32_t kSfCol = kAcc1 + 256;           // first column of the scales
+  static constexpr uint32_t kYBytes = 32 * 64 * 2;          // a warp's staged Y: two passes of 32 x 32
+  static constexpr uint32_t kYOff = kStages * kStagePitch;  // one per epilogue warp
   static constexpr uint32_t kWsOff = kYOff + 8 * kYBytes;   // weight scales of two tiles
   static constexpr uint32_t kBarOff = kWsOff + 2 * 256 * 4;
   static constexpr uint32_t kSmem = kBarOff + 1024 + 1024 /*align*/;
-  static constexpr uint32_t kSfCols = 12 * kAtoms;                 // A 4, B 8 per 512-byte tile of A
-  static constexpr uint32_t kSfSlots = kSfCols * 2 <= 64 ? 2 : 1;  // stages' scales held at once
-  static_assert(kSfCols * kSfSlots <= 64, "scale columns");
-  // K slices: three quarters of a 128 x 256 tile leave and as many arrive
-  static constexpr uint32_t kPartOff = 3 * 128 * 64 * 4;
+  static constexpr uint32_t kSfCols = 12 * kAtoms;  // A 4, B 8 per 512-byte tile of A
+  static_assert(kSfCol + 2 * kSfCols <= 512, "scale columns");
+  // K slices: six of a 128 x 256 tile's eight 32-column units leave at most,
+  // and as many arrive
+  static constexpr uint32_t kUnitBytes = 128 * 32 * 4;
+  static constexpr uint32_t kPartOff = 6 * kUnitBytes;
   static_assert(2 * kPartOff <= kWsOff, "partial sums reuse the ring and the staged Y");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 template <int BLOCK>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(Wide<BLOCK>::kThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
                 const __grid_constant__ CUtensorMap tmY, const MicroParams p) {
@@ -370,7 +407,7 @@ __global__ void __launch_bounds__(192, 1)
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
   uint64_t *empty = full + S;
   uint64_t *acc_full = empty + S;        // [2]: accumulator complete
-  uint64_t *shared_free = acc_full + 2;  // a tile's shared columns are in registers
+  uint64_t *shared_free = acc_full + 2;  // see the epilogue
   uint64_t *arrived = shared_free + 1;   // the other slices' sums
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(arrived + 1);
 
@@ -382,6 +419,7 @@ __global__ void __launch_bounds__(192, 1)
   const int tiles = p.tiles_m * p.tiles_n;
   const int s0 = static_cast<int>(static_cast<int64_t>(slice) * p.stages / p.slices);
   const int s1 = static_cast<int>(static_cast<int64_t>(slice + 1) * p.stages / p.slices);
+  const int u0 = slice * 8 / p.slices, u1 = (slice + 1) * 8 / p.slices;  // 32-column units this slice owns
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmW);
@@ -395,10 +433,10 @@ __global__ void __launch_bounds__(192, 1)
     }
     mbar_init(&acc_full[0], 1);
     mbar_init(&acc_full[1], 1);
-    mbar_init(shared_free, 256);  // both CTAs' epilogue threads
+    mbar_init(shared_free, 16);  // both CTAs' epilogue warps
     mbar_init(arrived, 1);
     fence_mbar_init();
-    mbar_arrive_expect_tx(arrived, (p.slices - 1) * (64 / p.slices) * 2048);
+    mbar_arrive_expect_tx(arrived, (p.slices - 1) * (u1 - u0) * C::kUnitBytes);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -406,7 +444,7 @@ __global__ void __launch_bounds__(192, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // the barriers of both CTAs exist before a remote arrive or load
+  cluster_meet();  // the barriers of both CTAs exist before a remote arrive or load
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
@@ -453,9 +491,9 @@ __global__ void __launch_bounds__(192, 1)
       int i = 0, j = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += step, ++j) {
-        if (j > 0 && !mbar_wait_cluster_warp(shared_free, static_cast<uint32_t>(j - 1) & 1u, p.status)) break;
+        if (j > 0 && !mbar_wait_warp(shared_free, static_cast<uint32_t>(j - 1) & 1u, p.status)) break;
         tc_fence_after();
-        const uint32_t d = tmem + (j & 1) * 192;
+        const uint32_t d = tmem + (j & 1) * C::kAcc1;
         for (int kb = s0; kb < s1; ++kb, ++i) {
           const int s = i % S;
           if (!mbar_wait_warp(&full[s], static_cast<uint32_t>(i / S) & 1u, p.status)) {
@@ -464,7 +502,7 @@ __global__ void __launch_bounds__(192, 1)
           }
           tc_fence_after();
           const uint32_t st = smem_addr(smem + s * C::kStagePitch);
-          const uint32_t sf = tmem + 448 + (C::kSfSlots == 2 ? (i & 1) * C::kSfCols : 0);
+          const uint32_t sf = tmem + C::kSfCol + (i & 1) * C::kSfCols;
           const uint32_t sfb = sf + 4 * C::kAtoms;
           const int steps = min(kStageK / kStepK, (p.K - kb * kStageK) / kStepK);
           if (leader) {
@@ -494,134 +532,156 @@ __global__ void __launch_bounds__(192, 1)
     }
     __syncwarp();
   } else if (p.slices == 1) {
-    const int e = warp - 2, q = warp & 3;
+    // The MMAs of tile j + 1 wait for all epilogue warps of both CTAs to
+    // arrive for tile j: the warps of the shared columns (half 0) once they
+    // hold tile j's, the others (half 1) once they have left tile j - 1, whose
+    // accumulator tile j + 1 takes.
+    const int e = warp - 2, half = e >> 2, q = warp & 3;
     float *wsm = reinterpret_cast<float *>(smem + C::kWsOff);
+    uint8_t *buf = smem + C::kYOff + e * C::kYBytes;
+    // one arrival a warp: 256 remote ones, a thread each, would queue
+    auto arrive = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(shared_free, lead));
+    };
     int j = 0;
-    uint32_t pass = 0;
     for (int t = first; t < tiles; t += step, ++j) {
       const int mq = (t % p.tiles_m) * 256 + static_cast<int>(rank) * 128 + q * 32, n0 = (t / p.tiles_m) * 256;
+      if (half == 1) arrive();
       float xsm = 1.0f;
       if (p.xs) xsm = __ldg(p.xs + (p.x_vec ? min(mq + lane, p.M - 1) : 0));
       // the tile's weight scales, in the buffer of the tile before last
       float *wt = wsm + (j & 1) * 256;
-      for (int k = static_cast<int>(threadIdx.x) - 64; k < 256; k += 128)
-        wt[k] = p.ws ? __ldg(p.ws + (p.w_vec ? min(n0 + k, p.N - 1) : 0)) : 1.0f;
-      named_bar_sync(1, 128);
+      const int k0 = static_cast<int>(threadIdx.x) - 64;
+      wt[k0] = p.ws ? __ldg(p.ws + (p.w_vec ? min(n0 + k0, p.N - 1) : 0)) : 1.0f;
+      named_bar_sync(1, 256);
       mbar_wait(&acc_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, p.status);
       tc_fence_after();
-      const uint32_t t_row = tmem + (j & 1) * 192 + (static_cast<uint32_t>(q * 32) << 16);
-      // 64 columns at a time, the shared ones first: the last of the lower
-      // accumulator, the first of the upper
-#pragma unroll 1
-      for (int h = 0; h < 4; ++h, ++pass) {
-        const int c = ((j & 1) ? h : (h + 3) & 3) * 64;
-        uint32_t v[64];
-        tmem_ld_32x32b_x64(t_row + c, v);
-        tmem_ld_wait();
-        tmem_regs_ready(v);
-        if (h == 0) {
-          tc_fence_before();
-          if (rank == 0)
-            mbar_arrive(shared_free);
-          else
-            mbar_arrive_cluster(mapa_shared(shared_free, lead));
-        }
-        uint8_t *buf = smem + C::kYOff + (2 * e + (pass & 1)) * C::kYBytes;
-        if (lane == 0) bulk_wait_group_read<1>();  // the store two passes ago has read it
+      // The 128 columns this warp takes, from c0 on: accumulator 0 shares its
+      // last 96, accumulator 1 its first 96.  v[0..2] are the shared ones (of
+      // half 0), v[3] the rest.
+      const int odd = j & 1, c0 = (half == 0) == (odd == 0) ? 128 : 0;
+      const int cs = c0 + (odd ? 0 : 32), cr = c0 + (odd ? 96 : 0);
+      const uint32_t t_row = tmem + odd * C::kAcc1 + (static_cast<uint32_t>(q * 32) << 16);
+      uint32_t v[4][32];
+      if (half == 1) named_bar_sync(2, 256);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) tmem_ld_32x32b_x32(t_row + cs + 32 * i, v[i]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 3; ++i) tmem_regs_ready(v[i]);
+      tc_fence_before();
+      if (half == 0) {
+        arrive();
+        named_bar_sync(2, 256);
+      }
+      tmem_ld_32x32b_x32(t_row + cr, v[3]);
+      tmem_ld_wait();
+      tmem_regs_ready(v[3]);
+      tc_fence_before();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = i < 3 ? cs + 32 * i : cr;
+        uint8_t *box = buf + (i & 1) * 2048;
+        if (lane == 0) bulk_wait_group_read<1>();  // the store before last has read the box
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 64; k += 8) {
+        for (int k = 0; k < 32; k += 8) {
           const float4 a = *reinterpret_cast<const float4 *>(wt + c + k), b = *reinterpret_cast<const float4 *>(wt + c + k + 4);
           const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
           uint32_t o[4];
 #pragma unroll
           for (int l = 0; l < 4; ++l)
-            o[l] = pack_bf16(__uint_as_float(v[k + 2 * l]) * (xsm * f[2 * l]),
-                             __uint_as_float(v[k + 2 * l + 1]) * (xsm * f[2 * l + 1]));
-          // row `lane` of the 128-byte swizzled box: 16-byte chunk i at i ^ (lane & 7)
-          *reinterpret_cast<uint4 *>(buf + lane * 128 + ((k / 8) ^ (lane & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+            o[l] = pack_bf16(__uint_as_float(v[i][k + 2 * l]) * (xsm * f[2 * l]),
+                             __uint_as_float(v[i][k + 2 * l + 1]) * (xsm * f[2 * l + 1]));
+          // row `lane` of the 64-byte swizzled box: 16-byte chunk i at i ^ (lane / 2 & 3)
+          *reinterpret_cast<uint4 *>(box + lane * 64 + ((k / 8) ^ (lane >> 1 & 3)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (mq < p.M && n0 + c < p.N) tma_store_2d(&tmY, buf, n0 + c, mq);
+          if (mq < p.M && n0 + c < p.N) tma_store_2d(&tmY, box, n0 + c, mq);
           bulk_commit_group();
         }
       }
     }
-    tc_fence_before();
-    if (lane == 0) bulk_wait_group_all();
+    // the CTA's shared memory outlives what the stores read; the writes are
+    // complete with the grid
+    if (lane == 0) bulk_wait_group_read<0>();
   }
   __syncwarp();
   if (p.slices > 1) {
-    // One tile per cluster.  Slice i owns 256 / slices columns of the tile;
-    // every slice lays the others' columns out [owner][4 columns][token] over
-    // its ring, copies them to their owners, and adds what arrives to its own,
-    // the other slices in order.
-    const int q = warp & 3, row = q * 32 + lane;
+    // One tile per cluster.  Slice i owns the 32-column units [8 i / slices,
+    // 8 (i + 1) / slices) of the tile; every slice lays the others' units out
+    // [unit][4 columns][token] over its ring, copies them to their owners, and
+    // adds what arrives to its own, the other slices in order.  The units are
+    // shared between the two halves of the epilogue warps.
+    const int half = (warp - 2) >> 2, q = warp & 3, row = q * 32 + lane;
     const int m = (first % p.tiles_m) * 256 + static_cast<int>(rank) * 128 + row, n0 = (first / p.tiles_m) * 256;
-    const int quads = 64 / p.slices;
     const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    float *wt = reinterpret_cast<float *>(smem + C::kWsOff);
+    float xsm = 1.0f;
     if (warp >= 2) {
+      if (p.xs) xsm = __ldg(p.xs + (p.x_vec ? min(m, p.M - 1) : 0));
+      const int k0 = static_cast<int>(threadIdx.x) - 64;
+      wt[k0] = p.ws ? __ldg(p.ws + (p.w_vec ? min(n0 + k0, p.N - 1) : 0)) : 1.0f;
       mbar_wait(&acc_full[0], 0u, p.status);
       tc_fence_after();
     }
     __syncwarp();
-    cluster_sync_all();  // no CTA's ring is in use any more
+    cluster_meet();  // no CTA's ring is in use any more
     if (warp >= 2) {
 #pragma unroll 1
-      for (int o = 0; o < p.slices; ++o) {
-        if (o == slice) continue;
-        uint8_t *mine = smem + (o - (o > slice ? 1 : 0)) * quads * 2048;
+      for (int i = 1; i < p.slices; ++i) {
+        const int o = (slice + i) % p.slices, o0 = o * 8 / p.slices, o1 = (o + 1) * 8 / p.slices;
+        uint8_t *mine = smem + (o > slice ? o0 - (u1 - u0) : o0) * C::kUnitBytes;
 #pragma unroll 1
-        for (int k = 0; k < quads; k += 8) {
+        for (int u = o0 + half; u < o1; u += 2) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(t_row + (o * quads + k) * 4, v);
+          tmem_ld_32x32b_x32(t_row + u * 32, v);
           tmem_ld_wait();
           tmem_regs_ready(v);
 #pragma unroll
           for (int l = 0; l < 8; ++l)
-            *reinterpret_cast<uint4 *>(mine + ((k + l) * 128 + row) * 16) =
+            *reinterpret_cast<uint4 *>(mine + (u - o0) * C::kUnitBytes + (l * 128 + row) * 16) =
                 make_uint4(v[4 * l], v[4 * l + 1], v[4 * l + 2], v[4 * l + 3]);
         }
         fence_proxy_async_smem();
-        named_bar_sync(1, 128);
+        named_bar_sync(1, 256);
         if (threadIdx.x == 64) {
           const uint32_t to = static_cast<uint32_t>(2 * o) + rank, from = slice - (slice > o ? 1 : 0);
-          bulk_push(mapa_shared(smem + C::kPartOff + from * quads * 2048, to), mine, quads * 2048, mapa_shared(arrived, to));
+          const uint32_t bytes = (o1 - o0) * C::kUnitBytes;
+          bulk_push(mapa_shared(smem + C::kPartOff + from * bytes, to), mine, bytes, mapa_shared(arrived, to));
         }
         __syncwarp();
       }
-      const float xsm = p.xs ? __ldg(p.xs + (p.x_vec ? min(m, p.M - 1) : 0)) : 1.0f;
-      const float w1 = p.ws && !p.w_vec ? __ldg(p.ws) : 1.0f;
-      mbar_wait_cluster(arrived, 0u, p.status);
-      const float4 *part = reinterpret_cast<const float4 *>(smem + C::kPartOff) + row;
+      mbar_wait(arrived, 0u, p.status);
 #pragma unroll 1
-      for (int k = 0; k < quads; k += 8) {
+      for (int u = u0 + half; u < u1; u += 2) {
+        const float4 *part = reinterpret_cast<const float4 *>(smem + C::kPartOff + (u - u0) * C::kUnitBytes) + row;
         uint32_t v[32];
-        tmem_ld_32x32b_x32(t_row + (slice * quads + k) * 4, v);
+        tmem_ld_32x32b_x32(t_row + u * 32, v);
         tmem_ld_wait();
         tmem_regs_ready(v);
 #pragma unroll
         for (int l = 0; l < 8; l += 2) {
-          const int n = n0 + (slice * quads + k + l) * 4;
+          const int c = u * 32 + l * 4;
           float f[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[4 * l + i]);
 #pragma unroll
-          for (int r = 0; r < 3; ++r) {
+          for (int r = 0; r < kMaxWideSlices - 1; ++r) {
             if (r < p.slices - 1) {
-              const float4 a = part[(r * quads + k + l) * 128], b = part[(r * quads + k + l + 1) * 128];
+              const float4 *src = part + r * (u1 - u0) * (C::kUnitBytes / 16);
+              const float4 a = src[l * 128], b = src[(l + 1) * 128];
               f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w, f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
             }
           }
-          if (n < p.N && m < p.M) {
-            float4 a = make_float4(w1, w1, w1, w1), b = a;
-            if (p.w_vec) a = __ldg(reinterpret_cast<const float4 *>(p.ws + n)), b = __ldg(reinterpret_cast<const float4 *>(p.ws + n + 4));
-            *reinterpret_cast<uint4 *>(p.y + static_cast<int64_t>(m) * p.N + n) = make_uint4(
-                pack_bf16(f[0] * (xsm * a.x), f[1] * (xsm * a.y)), pack_bf16(f[2] * (xsm * a.z), f[3] * (xsm * a.w)),
-                pack_bf16(f[4] * (xsm * b.x), f[5] * (xsm * b.y)), pack_bf16(f[6] * (xsm * b.z), f[7] * (xsm * b.w)));
-          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= xsm * wt[c + i];
+          if (n0 + c < p.N && m < p.M)
+            *reinterpret_cast<uint4 *>(p.y + static_cast<int64_t>(m) * p.N + n0 + c) =
+                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
         }
       }
       tc_fence_before();
@@ -632,7 +692,7 @@ __global__ void __launch_bounds__(192, 1)
   __syncthreads();
   // no CTA frees tensor memory or leaves while another may still use it or
   // arrive on its barriers
-  cluster_sync_all();
+  cluster_meet();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
@@ -641,24 +701,25 @@ __global__ void __launch_bounds__(192, 1)
 
 // ------------------------------------------------------------------ host
 
-// Clusters of `size` CTAs of the wide kernel that the device runs at once.
+// Clusters of `slices` SM pairs of the wide kernel that the device runs at once
+// (148 SMs hold 74, 33, 22 and 15).
 template <int BLOCK>
-int wide_clusters(int size) {
-  static int cap[3] = {0, 0, 0};
+int wide_clusters(int slices) {
+  static int cap[kMaxWideSlices + 1] = {};
   static std::once_flag once;
   std::call_once(once, [] {
     if (cudaFuncSetAttribute(wide_kernel<BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<BLOCK>::kSmem) != cudaSuccess) {
       (void)cudaGetLastError();
       return;
     }
-    for (int i = 0; i < 3; ++i) {
+    for (unsigned i = 1; i <= kMaxWideSlices; ++i) {
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2u << i, 1, 1);
-      cfg.blockDim = dim3(192, 1, 1);
+      cfg.gridDim = dim3(2 * i, 1, 1);
+      cfg.blockDim = dim3(Wide<BLOCK>::kThreads, 1, 1);
       cfg.dynamicSmemBytes = Wide<BLOCK>::kSmem;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = 2u << i;
+      at[0].val.clusterDim.x = 2 * i;
       at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
       cfg.attrs = at;
       cfg.numAttrs = 1;
@@ -669,14 +730,15 @@ int wide_clusters(int size) {
         (void)cudaGetLastError();
     }
   });
-  return cap[size == 2 ? 0 : size == 4 ? 1 : 2];
+  return cap[slices];
 }
 
 template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), unsigned grid, unsigned cluster, uint32_t smem, cudaStream_t st, Args... args) {
+cudaError_t launch(void (*kernel)(Args...), unsigned grid, unsigned cluster, unsigned threads, uint32_t smem, cudaStream_t st,
+                   Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(192, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
@@ -712,10 +774,10 @@ cudaError_t launch_narrow(const MicroGemmArgs &a, MicroParams p, cudaStream_t st
   if (err != cudaSuccess) return err;
   p.tiles_n = (a.N + 127) / 128;
   p.tiles_m = (a.M + BN - 1) / BN;
-  // K slices: as many as leave every CTA resident at once (one
-  // token tile at most 128 wide, so a tile starts at a band of 128 rows)
+  // K slices: as many as leave every CTA resident at once, one or two on an SM
+  // (clusters of 3 to 8 fill 132 of the 148 SMs)
   const int64_t tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_m;
-  int64_t s = C::kPerSm * 148 / tiles;
+  int64_t s = (C::kPerSm > 1 ? 264 : 132) / tiles;
   s = s < 1 ? 1 : s > kMaxSlices ? kMaxSlices : s;
   if (s > p.stages) s = p.stages;
   p.slices = static_cast<int>(s);
@@ -723,8 +785,8 @@ cudaError_t launch_narrow(const MicroGemmArgs &a, MicroParams p, cudaStream_t st
   if (!make_maps(&tm[0], &tm[2], a.wq, a.wb, a.N, a.K, BLOCK, 128) ||
       !make_maps(&tm[1], &tm[3], a.xq, a.xb, a.M, a.K, BLOCK, BN))
     return cudaErrorInvalidValue;
-  return launch(narrow_kernel<BLOCK, BN>, static_cast<unsigned>(tiles * s), static_cast<unsigned>(s), C::kSmem, st, tm[0], tm[1],
-                tm[2], tm[3], p);
+  return launch(narrow_kernel<BLOCK, BN>, static_cast<unsigned>(tiles * s), static_cast<unsigned>(s), 192, C::kSmem, st, tm[0],
+                tm[1], tm[2], tm[3], p);
 }
 
 template <int BLOCK>
@@ -733,20 +795,27 @@ cudaError_t launch_wide(const MicroGemmArgs &a, MicroParams p, cudaStream_t st) 
   p.tiles_n = (a.N + 255) / 256;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  const int pairs = wide_clusters<BLOCK>(2);
+  const int pairs = wide_clusters<BLOCK>(1);
   if (pairs < 1) return cudaErrorInvalidConfiguration;
-  // few tiles: slices of K over the idle pairs
+  // few tiles: slices of K over the idle pairs.  A stage takes about 0.4 us
+  // and a join about 3 us, as much as 8 stages.
   int s = 1;
-  while (s < 4 && tiles * 2 * s <= pairs && 2 * s <= p.stages && wide_clusters<BLOCK>(4 * s) >= 1) s *= 2;
+  int64_t best = (tiles + pairs - 1) / pairs * p.stages;
+  for (int i = 2; i <= kMaxWideSlices && i <= p.stages; ++i) {
+    const int cap = wide_clusters<BLOCK>(i);
+    if (cap < 1) break;
+    const int64_t cost = (tiles + cap - 1) / cap * ((p.stages + i - 1) / i + 8);
+    if (cost < best) best = cost, s = i;
+  }
   p.slices = s;
   const int64_t clusters = s > 1 ? tiles : (tiles < pairs ? tiles : pairs);
   CUtensorMap tm[5];
   if (!make_maps(&tm[0], &tm[2], a.wq, a.wb, a.N, a.K, BLOCK, 128) ||
       !make_maps(&tm[1], &tm[3], a.xq, a.xb, a.M, a.K, BLOCK, 128) ||
-      !make_tensor_map_2d(&tm[4], a.y, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.N, a.M, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+      !make_tensor_map_2d(&tm[4], a.y, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.N, a.M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  return launch(wide_kernel<BLOCK>, static_cast<unsigned>(clusters * 2 * s), static_cast<unsigned>(2 * s), Wide<BLOCK>::kSmem,
-                st, tm[0], tm[1], tm[2], tm[3], tm[4], p);
+  return launch(wide_kernel<BLOCK>, static_cast<unsigned>(clusters * 2 * s), static_cast<unsigned>(2 * s), Wide<BLOCK>::kThreads,
+                Wide<BLOCK>::kSmem, st, tm[0], tm[1], tm[2], tm[3], tm[4], p);
 }
 
 template <int BLOCK>
