@@ -602,11 +602,16 @@ def fp8_gemm_dense(xq: torch.Tensor, x_scale, wq: torch.Tensor, w_scale,
 # Block-scaled FP4, and the row stages of a block with quantised outputs
 # ---------------------------------------------------------------------------
 
-_FP4 = {"nvfp4": _lib.FP4_NVFP4, "mxfp4": _lib.FP4_MXFP4}
-_FP4_BLOCK = {"nvfp4": 16, "mxfp4": 32}
+# These calls are short on the device (2 to 10 us for a decoded token), so the
+# binding keeps the host's part short too: a call's checks read each tensor
+# once, and the stream is taken as a raw handle.
+_FP4 = {"nvfp4": (_lib.FP4_NVFP4, 16), "mxfp4": (_lib.FP4_MXFP4, 32)}
+_U8, _BF16, _F32 = torch.uint8, torch.bfloat16, torch.float32
+_empty = torch.empty
 
 
-def _fp4_format(format: str) -> int:
+def _fp4_format(format: str):
+    """(code, block) of a format's name."""
     try:
         return _FP4[format]
     except (KeyError, TypeError):
@@ -614,9 +619,13 @@ def _fp4_format(format: str) -> int:
 
 
 def _bf16_rows(t, name):
-    if t.dtype != torch.bfloat16 or t.dim() != 2:
+    """(rows, columns, device) of a call's first operand."""
+    if t.dtype != _BF16 or t.dim() != 2:
         raise Sp24Error(f"{name} must be a 2-D bf16 tensor")
-    return t.shape
+    if not t.is_cuda or not t.is_contiguous():
+        raise Sp24Error("tensors must be contiguous CUDA tensors")
+    rows, cols = t.shape
+    return rows, cols, t.device
 
 
 def _operand(t, name, dtype, numel, device):
@@ -625,55 +634,78 @@ def _operand(t, name, dtype, numel, device):
         raise Sp24Error(f"{name} has the wrong shape or dtype")
     if t.device != device or not t.is_contiguous():
         raise Sp24Error(f"{name} must be contiguous and on {device}")
-    return t
+    return t.data_ptr()
 
 
 def _row_status(status, device):
-    return None if status is None else _operand(status, "status", torch.int32, 1, device).data_ptr()
+    return None if status is None else _operand(status, "status", torch.int32, 1, device)
 
 
 def _call(name, device, *args):
     """One library call on `device`'s current stream, with that device current."""
     fn = getattr(_lib.load(), name)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(device))
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, _stream(device))
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc:
         _lib.check(rc, name)
 
 
-def fp4_block_scales_size(rows: int, cols: int, format: str = "nvfp4") -> int:
-    """Bytes of the block-scale tiles of a [rows, cols] matrix."""
-    block = _FP4_BLOCK[format] if _fp4_format(format) >= 0 else 0
+def _tiles_size(rows, cols, block):
     return (rows + 127) // 128 * ((cols // block + 3) // 4) * 512
 
 
-def _fp4_outputs(rows, cols, format, device, out):
-    """(q, block_scales, row_scales) to write: those of ``out``, new ones where it has none."""
-    out = out or {}
-    size = fp4_block_scales_size(rows, cols, format)
-    q, blocks, scales = out.get("q"), out.get("block_scales"), out.get("row_scales")
-    q = (torch.empty((rows, cols // 2), dtype=torch.uint8, device=device) if q is None
-         else _operand(q, "q", torch.uint8, rows * (cols // 2), device))
-    blocks = (torch.empty(size, dtype=torch.uint8, device=device) if blocks is None
-              else _operand(blocks, "block_scales", torch.uint8, size, device))
-    if format == "mxfp4":
-        return q, blocks, None
-    scales = (torch.empty(rows, dtype=torch.float32, device=device) if scales is None
-              else _operand(scales, "row_scales", torch.float32, rows, device))
-    return q, blocks, scales
+def fp4_block_scales_size(rows: int, cols: int, format: str = "nvfp4") -> int:
+    """Bytes of the block-scale tiles of a [rows, cols] matrix."""
+    return _tiles_size(rows, cols, _fp4_format(format)[1])
+
+
+def _fp4_outputs(rows, cols, fmt, device, out):
+    """(q, block_scales, row_scales) to write and their pointers: those of
+    ``out``, new ones where it has none."""
+    code, block = fmt
+    size = _tiles_size(rows, cols, block)
+    q = blocks = scales = None
+    if out:
+        q, blocks, scales = out.get("q"), out.get("block_scales"), out.get("row_scales")
+    if q is None:
+        q = _empty((rows, cols // 2), dtype=_U8, device=device)
+        qp = q.data_ptr()
+    else:
+        qp = _operand(q, "q", _U8, rows * (cols // 2), device)
+    if blocks is None:
+        blocks = _empty(size, dtype=_U8, device=device)
+        bp = blocks.data_ptr()
+    else:
+        bp = _operand(blocks, "block_scales", _U8, size, device)
+    if code == _lib.FP4_MXFP4:
+        return (q, blocks, None), qp, bp, None
+    if scales is None:
+        scales = _empty(rows, dtype=_F32, device=device)
+        sp = scales.data_ptr()
+    else:
+        sp = _operand(scales, "row_scales", _F32, rows, device)
+    return (q, blocks, scales), qp, bp, sp
 
 
 def _fp8_outputs(rows, cols, device, out):
-    out = out or {}
-    q, scales = out.get("q"), out.get("scales")
-    q = (torch.empty((rows, cols), dtype=torch.uint8, device=device) if q is None
-         else _operand(q, "q", torch.uint8, rows * cols, device))
-    scales = (torch.empty(rows, dtype=torch.float32, device=device) if scales is None
-              else _operand(scales, "scales", torch.float32, rows, device))
-    return q, scales
+    q = scales = None
+    if out:
+        q, scales = out.get("q"), out.get("scales")
+    if q is None:
+        q = _empty((rows, cols), dtype=_U8, device=device)
+        qp = q.data_ptr()
+    else:
+        qp = _operand(q, "q", _U8, rows * cols, device)
+    if scales is None:
+        scales = _empty(rows, dtype=_F32, device=device)
+        sp = scales.data_ptr()
+    else:
+        sp = _operand(scales, "scales", _F32, rows, device)
+    return q, scales, qp, sp
 
 
 def fp4_quantize_microscaled(X: torch.Tensor, format: str = "nvfp4", status: torch.Tensor | None = None,
@@ -685,27 +717,27 @@ def fp4_quantize_microscaled(X: torch.Tensor, format: str = "nvfp4", status: tor
     cols / 2], block_scales u8 in the header's tile order, row_scales f32
     [rows] or None for mxfp4); ``out`` may supply any of these preallocated.
     """
-    _require_cuda(X)
     fmt = _fp4_format(format)
-    rows, cols = _bf16_rows(X, "X")
-    dev = X.device
-    q, blocks, scales = _fp4_outputs(rows, cols, format, dev, out)
-    _call("fp4_quantize_microscaled", dev, X.data_ptr(), rows, cols, fmt, q.data_ptr(), blocks.data_ptr(),
-          _ptr(scales), _row_status(status, dev))
-    return q, blocks, scales
+    rows, cols, dev = _bf16_rows(X, "X")
+    res, qp, bp, sp = _fp4_outputs(rows, cols, fmt, dev, out)
+    _call("fp4_quantize_microscaled", dev, X.data_ptr(), rows, cols, fmt[0], qp, bp, sp, _row_status(status, dev))
+    return res
 
 
 def fp4_unpack_e4m3(q: torch.Tensor, out: torch.Tensor | None = None):
     """The E4M3 codes (u8 [rows, cols], exact) of FP4 codes q u8 [rows, cols / 2]."""
-    _require_cuda(q)
-    if q.dtype != torch.uint8 or q.dim() != 2:
+    if q.dtype != _U8 or q.dim() != 2:
         raise Sp24Error("q must be a 2-D uint8 tensor of packed FP4 codes")
-    rows, cols = q.shape[0], 2 * q.shape[1]
+    _require_cuda(q)
+    rows, half = q.shape
     dev = q.device
-    o = (torch.empty((rows, cols), dtype=torch.uint8, device=dev) if out is None
-         else _operand(out, "out", torch.uint8, rows * cols, dev))
-    _call("fp4_unpack_e4m3", dev, q.data_ptr(), rows, cols, o.data_ptr())
-    return o
+    if out is None:
+        out = _empty((rows, 2 * half), dtype=_U8, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _operand(out, "out", _U8, rows * 2 * half, dev)
+    _call("fp4_unpack_e4m3", dev, q.data_ptr(), rows, 2 * half, op)
+    return out
 
 
 def _row_scales(t, name, count, device):
@@ -715,7 +747,7 @@ def _row_scales(t, name, count, device):
     n = t.numel()
     if n != 1 and n != count:
         raise Sp24Error(f"{name} must hold one value or one per row")
-    return _operand(t, name, torch.float32, n, device).data_ptr(), int(n != 1)
+    return _operand(t, name, _F32, n, device), int(n != 1)
 
 
 def fp4_gemm_microscaled(xq: torch.Tensor, x_block_scales: torch.Tensor, x_scales, wq: torch.Tensor,
@@ -724,36 +756,41 @@ def fp4_gemm_microscaled(xq: torch.Tensor, x_block_scales: torch.Tensor, x_scale
     """Y bf16 [M, N] = x . w^T of two block-scaled FP4 matrices: xq u8 [M, K/2] and
     wq u8 [N, K/2] with the block scales of fp4_quantize_microscaled; x_scales
     and w_scales hold one value per row, one for all, or are None (1)."""
-    _require_cuda(xq)
-    fmt = _fp4_format(format)
-    if xq.dtype != torch.uint8 or xq.dim() != 2 or wq.dim() != 2:
+    code, block = _fp4_format(format)
+    if xq.dtype != _U8 or xq.dim() != 2 or wq.dim() != 2:
         raise Sp24Error("xq and wq must be 2-D uint8 tensors of packed FP4 codes")
-    m, n, k, dev = xq.shape[0], wq.shape[0], 2 * xq.shape[1], xq.device
-    _operand(wq, "wq", torch.uint8, n * (k // 2), dev)
-    _operand(x_block_scales, "x_block_scales", torch.uint8, fp4_block_scales_size(m, k, format), dev)
-    _operand(w_block_scales, "w_block_scales", torch.uint8, fp4_block_scales_size(n, k, format), dev)
+    _require_cuda(xq)
+    m, half = xq.shape
+    n, dev = wq.shape[0], xq.device
+    wp = _operand(wq, "wq", _U8, n * half, dev)
+    xb = _operand(x_block_scales, "x_block_scales", _U8, _tiles_size(m, 2 * half, block), dev)
+    wb = _operand(w_block_scales, "w_block_scales", _U8, _tiles_size(n, 2 * half, block), dev)
     xs, x_vec = _row_scales(x_scales, "x_scales", m, dev)
     ws, w_vec = _row_scales(w_scales, "w_scales", n, dev)
-    y = (torch.empty((m, n), dtype=torch.bfloat16, device=dev) if out is None
-         else _operand(out, "out", torch.bfloat16, m * n, dev))
-    _call("fp4_gemm_microscaled", dev, xq.data_ptr(), x_block_scales.data_ptr(), xs, x_vec, wq.data_ptr(),
-          w_block_scales.data_ptr(), ws, w_vec, fmt, y.data_ptr(), m, n, k, _row_status(status, dev))
-    return y
+    if out is None:
+        out = _empty((m, n), dtype=_BF16, device=dev)
+        yp = out.data_ptr()
+    else:
+        yp = _operand(out, "out", _BF16, m * n, dev)
+    _call("fp4_gemm_microscaled", dev, xq.data_ptr(), xb, xs, x_vec, wp, wb, ws, w_vec, code, yp, m, n, 2 * half,
+          _row_status(status, dev))
+    return out
 
 
 def _norm_inputs(X, weight, residual, residual_out):
-    _require_cuda(X)
-    rows, cols = _bf16_rows(X, "X")
-    dev = X.device
-    _operand(weight, "weight", torch.bfloat16, cols, dev)
+    rows, cols, dev = _bf16_rows(X, "X")
+    wp = _operand(weight, "weight", _BF16, cols, dev)
     if residual is None:
         if residual_out is not None:
             raise Sp24Error("residual_out needs a residual")
-        return rows, cols, dev, None
-    _operand(residual, "residual", torch.bfloat16, rows * cols, dev)
-    h = (torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if residual_out is None
-         else _operand(residual_out, "residual_out", torch.bfloat16, rows * cols, dev))
-    return rows, cols, dev, h
+        return rows, cols, dev, wp, None, None, X
+    rp = _operand(residual, "residual", _BF16, rows * cols, dev)
+    if residual_out is None:
+        residual_out = torch.empty_like(X)
+        hp = residual_out.data_ptr()
+    else:
+        hp = _operand(residual_out, "residual_out", _BF16, rows * cols, dev)
+    return rows, cols, dev, wp, rp, hp, residual_out
 
 
 def fp8_rmsnorm_quantize_pertoken(X: torch.Tensor, weight: torch.Tensor, eps: float,
@@ -763,11 +800,11 @@ def fp8_rmsnorm_quantize_pertoken(X: torch.Tensor, weight: torch.Tensor, eps: fl
     [rows, cols], scales f32 [rows], h bf16 [rows, cols]); without a residual h
     is X itself.  residual_out may be X or residual (in place); ``out`` may
     supply q and scales."""
-    rows, cols, dev, h = _norm_inputs(X, weight, residual, residual_out)
-    q, scales = _fp8_outputs(rows, cols, dev, out)
-    _call("fp8_rmsnorm_quantize_pertoken", dev, X.data_ptr(), _ptr(residual), weight.data_ptr(), eps, rows, cols,
-          _ptr(h), q.data_ptr(), scales.data_ptr(), _row_status(status, dev))
-    return q, scales, X if h is None else h
+    rows, cols, dev, wp, rp, hp, h = _norm_inputs(X, weight, residual, residual_out)
+    q, scales, qp, sp = _fp8_outputs(rows, cols, dev, out)
+    _call("fp8_rmsnorm_quantize_pertoken", dev, X.data_ptr(), rp, wp, eps, rows, cols, hp, qp, sp,
+          _row_status(status, dev))
+    return q, scales, h
 
 
 def fp4_rmsnorm_quantize_microscaled(X: torch.Tensor, weight: torch.Tensor, eps: float, format: str = "nvfp4",
@@ -778,28 +815,26 @@ def fp4_rmsnorm_quantize_microscaled(X: torch.Tensor, weight: torch.Tensor, eps:
     returns (q, block_scales, row_scales, h), the first three as
     fp4_quantize_microscaled, h as fp8_rmsnorm_quantize_pertoken."""
     fmt = _fp4_format(format)
-    rows, cols, dev, h = _norm_inputs(X, weight, residual, residual_out)
-    q, blocks, scales = _fp4_outputs(rows, cols, format, dev, out)
-    _call("fp4_rmsnorm_quantize_microscaled", dev, X.data_ptr(), _ptr(residual), weight.data_ptr(), eps, rows, cols,
-          fmt, _ptr(h), q.data_ptr(), blocks.data_ptr(), _ptr(scales), _row_status(status, dev))
-    return q, blocks, scales, X if h is None else h
+    rows, cols, dev, wp, rp, hp, h = _norm_inputs(X, weight, residual, residual_out)
+    res, qp, bp, sp = _fp4_outputs(rows, cols, fmt, dev, out)
+    _call("fp4_rmsnorm_quantize_microscaled", dev, X.data_ptr(), rp, wp, eps, rows, cols, fmt[0], hp, qp, bp, sp,
+          _row_status(status, dev))
+    return *res, h
 
 
 def _gated_rows(GU):
-    _require_cuda(GU)
-    rows, both = _bf16_rows(GU, "GU")
+    rows, both, dev = _bf16_rows(GU, "GU")
     if both % 2:
         raise Sp24Error("GU must hold as many gate as up columns")
-    return rows, both // 2, GU.device
+    return rows, both // 2, dev
 
 
 def fp8_silu_mul_quantize_pertoken(GU: torch.Tensor, status: torch.Tensor | None = None, out: dict | None = None):
     """silu(gate) * up of GU bf16 [rows, 2 cols] (gate columns, then up columns)
     with E4M3 output: returns (q u8 [rows, cols], scales f32 [rows])."""
     rows, cols, dev = _gated_rows(GU)
-    q, scales = _fp8_outputs(rows, cols, dev, out)
-    _call("fp8_silu_mul_quantize_pertoken", dev, GU.data_ptr(), rows, cols, q.data_ptr(), scales.data_ptr(),
-          _row_status(status, dev))
+    q, scales, qp, sp = _fp8_outputs(rows, cols, dev, out)
+    _call("fp8_silu_mul_quantize_pertoken", dev, GU.data_ptr(), rows, cols, qp, sp, _row_status(status, dev))
     return q, scales
 
 
@@ -809,10 +844,10 @@ def fp4_silu_mul_quantize_microscaled(GU: torch.Tensor, format: str = "nvfp4", s
     returns (q, block_scales, row_scales) as fp4_quantize_microscaled."""
     fmt = _fp4_format(format)
     rows, cols, dev = _gated_rows(GU)
-    q, blocks, scales = _fp4_outputs(rows, cols, format, dev, out)
-    _call("fp4_silu_mul_quantize_microscaled", dev, GU.data_ptr(), rows, cols, fmt, q.data_ptr(), blocks.data_ptr(),
-          _ptr(scales), _row_status(status, dev))
-    return q, blocks, scales
+    res, qp, bp, sp = _fp4_outputs(rows, cols, fmt, dev, out)
+    _call("fp4_silu_mul_quantize_microscaled", dev, GU.data_ptr(), rows, cols, fmt[0], qp, bp, sp,
+          _row_status(status, dev))
+    return res
 
 
 def debug_e4m3_encode(v: torch.Tensor) -> torch.Tensor:

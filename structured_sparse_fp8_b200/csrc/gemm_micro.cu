@@ -15,8 +15,8 @@
 // hold does not matter, and a row's scales only ever reach that row's results.
 //
 // Two kernels:
-//   narrow (M <= 128 tokens): the weights are the MMA's A operand (128 rows),
-//     the tokens its B operand (BN columns), one CTA per weight tile and K
+//   narrow (up to 64 tokens, or few tiles): the weights are the MMA's A operand
+//     (128 rows), the tokens its B operand (BN columns), one CTA per tile and K
 //     slice.  Such calls stream the weights, so K is sliced over a cluster of
 //     CTAs until the SMs are full; the slices' partial sums meet in shared
 //     memory over the cluster (distributed shared memory), are added in slice
@@ -44,7 +44,8 @@ constexpr int kStageK = 256;            // K elements per pipeline stage
 constexpr int kRowBytes = kStageK / 2;  // one swizzled row of codes
 constexpr int kStepK = 64;              // K per MMA
 constexpr int kMaxSlices = 8;           // CTAs that share a narrow tile's K (a portable cluster)
-constexpr int kMaxWideSlices = 4;       // SM pairs that share a wide tile's K
+constexpr int kMaxWideSlices = 3;       // SM pairs that share a wide tile's K
+constexpr int kNarrowTiles = 132;       // SMs that clusters of several CTAs fill
 
 // Instruction descriptor of kinds mxf4 / mxf4nvf4: E2M1 operands (1), both
 // K-major; scale type UE4M3 (0) or UE8M0 (1) at bit 23; N >> 3 at 17, M >> 7
@@ -160,8 +161,8 @@ struct Narrow {
   // CTAs that share an SM.  The smallest tiles leave room for the next call's
   // CTAs, whose start (barriers, tensor memory, descriptors: about 1 us) then
   // hides behind this call.
-  static constexpr int kPerSm = BN <= 16 ? 4 : BN <= 32 ? 3 : BN <= 64 ? 2 : 1;
-  static constexpr uint32_t kBudget = kPerSm == 4 ? 57344 : kPerSm == 3 ? 75776 : kPerSm == 2 ? 114688 : 204800;
+  static constexpr int kPerSm = BN <= 16 ? 4 : BN <= 32 ? 3 : 2;
+  static constexpr uint32_t kBudget = kPerSm == 4 ? 57344 : kPerSm == 3 ? 75776 : 114688;
   static constexpr int kStages = (kBudget - 3072 - (kOwnRoom ? kPartBytes : 0)) / kStageBytes;
   static constexpr uint32_t kPartOff = kOwnRoom ? kStages * kStageBytes : BN * 512;
   static constexpr uint32_t kBarOff = kStages * kStageBytes + (kOwnRoom ? kPartBytes : 0);
@@ -169,8 +170,9 @@ struct Narrow {
   static constexpr uint32_t kSmem = kScaleOff + 512 + 1024 /*align*/;
   static constexpr uint32_t kSfCols = 8 * kAtoms;  // A's and B's scales of a stage; two stages' worth
   static constexpr uint32_t kTmemNeed = BN + 2 * kSfCols;
-  static constexpr uint32_t kTmemCols = kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128 : 256;
-  static_assert(kStageBytes % 1024 == 0 && BN % 16 == 0 && BN <= 128, "tile");
+  static constexpr uint32_t kTmemCols = kTmemNeed <= 64 ? 64 : 128;
+  static_assert(kTmemNeed <= 128 && kPerSm * kTmemCols <= 512, "tensor memory");
+  static_assert(kStageBytes % 1024 == 0 && BN % 16 == 0 && BN <= 64, "tile");
   static_assert(kStages >= 2 && BN * 512 + (kOwnRoom ? 0 : kPartBytes) <= kStages * kStageBytes, "sums fit the ring");
 };
 
@@ -253,6 +255,9 @@ __global__ void __launch_bounds__(192, Narrow<BLOCK, BN>::kPerSm)
       tc_fence_after();
       const uint32_t st = smem_addr(smem + s * C::kStageBytes);
       const uint32_t sfa = tmem + BN + (i & 1) * C::kSfCols, sfb = sfa + 4 * C::kAtoms;
+      // a second tile of 64 tokens starts in the middle of a band of scales
+      // (32 rows to a column)
+      const uint32_t sfb_m = sfb + (m0 % 128) / 32;
       const int steps = min(kStageK / kStepK, (p.K - kb * kStageK) / kStepK);
       if (leader) {
 #pragma unroll
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(192, Narrow<BLOCK, BN>::kPerSm)
           const uint64_t bd = smem_desc(st + C::kBOff + 32 * j, 16, 8 * kRowBytes, kSwizzle128B);
           const uint32_t col = BLOCK == 16 ? 4 * j : 4 * (j / 2);
           const uint32_t id = BLOCK == 16 ? 0u : 2u * (j & 1);
-          mma_micro<BLOCK, false>(tmem, ad, bd, idesc | id << 4 | id << 29, sfa + col, sfb + col, (i | j) ? 1u : 0u);
+          mma_micro<BLOCK, false>(tmem, ad, bd, idesc | id << 4 | id << 29, sfa + col, sfb_m + col, (i | j) ? 1u : 0u);
         }
         mma_commit(&empty[s]);
       }
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(Wide<BLOCK>::kThreads, 1)
 // ------------------------------------------------------------------ host
 
 // Clusters of `slices` SM pairs of the wide kernel that the device runs at once
-// (148 SMs hold 74, 33, 22 and 15).
+// (148 SMs hold 74, 33 and 22).
 template <int BLOCK>
 int wide_clusters(int slices) {
   static int cap[kMaxWideSlices + 1] = {};
@@ -774,10 +779,10 @@ cudaError_t launch_narrow(const MicroGemmArgs &a, MicroParams p, cudaStream_t st
   if (err != cudaSuccess) return err;
   p.tiles_n = (a.N + 127) / 128;
   p.tiles_m = (a.M + BN - 1) / BN;
-  // K slices: as many as leave every CTA resident at once, one or two on an SM
-  // (clusters of 3 to 8 fill 132 of the 148 SMs)
+  // K slices: as many as leave every CTA resident at once, two on an SM
+  // (clusters of 3 to 8 CTAs fill 132 of the 148)
   const int64_t tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_m;
-  int64_t s = (C::kPerSm > 1 ? 264 : 132) / tiles;
+  int64_t s = 2 * kNarrowTiles / tiles;
   s = s < 1 ? 1 : s > kMaxSlices ? kMaxSlices : s;
   if (s > p.stages) s = p.stages;
   p.slices = static_cast<int>(s);
@@ -833,8 +838,12 @@ cudaError_t launch_block(const MicroGemmArgs &a, cudaStream_t st) {
   p.status = a.status;
   if (a.M <= 16) return launch_narrow<BLOCK, 16>(a, p, st);
   if (a.M <= 32) return launch_narrow<BLOCK, 32>(a, p, st);
-  if (a.M <= 64) return launch_narrow<BLOCK, 64>(a, p, st);
-  if (a.M <= 128) return launch_narrow<BLOCK, 128>(a, p, st);
+  // More than 64 tokens: narrow tiles as long as two or more slices of K fit
+  // (nvfp4, cold: 256 x 4096 x 4096, 128 tiles, 9.2 us against 11.7 on SM
+  // pairs; 384 x 4096 x 4096, 192 tiles, 12.2 against 10.6; 256 x 4096 x 512
+  // 5.6 against 4.9).
+  const int64_t tiles = static_cast<int64_t>((a.N + 127) / 128) * ((a.M + 63) / 64);
+  if (a.M <= 64 || tiles <= kNarrowTiles) return launch_narrow<BLOCK, 64>(a, p, st);
   return launch_wide<BLOCK>(a, p, st);
 }
 

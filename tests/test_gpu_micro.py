@@ -359,7 +359,8 @@ def check_product(y, xv, wv, xs, ws):
 
 PSHAPES = [(1, 8, 64), (1, 128, 256), (2, 136, 192), (3, 4104, 320), (8, 256, 4096), (16, 1000, 1024), (17, 512, 2112),
            (33, 384, 1024), (64, 2048, 512), (100, 264, 4160), (128, 4096, 448), (129, 520, 832), (256, 1024, 1088),
-           (300, 2304, 2048), (515, 1160, 576), (1000, 520, 4160), (2050, 1032, 704), (1, 11008, 4096), (1, 96, 28672)]
+           (300, 2304, 2048), (515, 1160, 576), (1000, 520, 4160), (2050, 1032, 704), (1, 11008, 4096), (1, 96, 28672),
+           (70, 9000, 576), (200, 4360, 5120), (250, 6152, 5184), (600, 4104, 4160), (2000, 4096, 1024), (3000, 6152, 320)]
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
