@@ -72,9 +72,21 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+// max(a, |b|, |c|), a >= 0
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+// 1 / v to one step, v a normal number
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 __device__ __forceinline__ float warp_sum(float v) {
@@ -82,11 +94,11 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-__device__ __forceinline__ float max_abs8(const float *y) {
-  float m = fabsf(y[0]);
+// The largest of `so_far` (>= 0) and the chunk's magnitudes.
+__device__ __forceinline__ float max_abs8(const float *y, float so_far = 0.0f) {
 #pragma unroll
-  for (int i = 1; i < kChunk; ++i) m = max_nan(m, fabsf(y[i]));
-  return m;
+  for (int i = 0; i < kChunk; i += 2) so_far = max_abs3(so_far, y[i], y[i + 1]);
+  return so_far;
 }
 
 // What chunk `c` of the row contributes: y, or z = h * w for the norm (then
@@ -136,8 +148,8 @@ __device__ __forceinline__ void chunk_values(const RowQuantArgs &p, int64_t row,
 // How a row's values become codes: one factor for the row (E4M3), or R.
 struct RowScale {
   float pre;   // factor for values of a row so small that its quotients would leave fp32's range, else 1
-  float mul;   // E4M3: codes are E4M3(value * mul); mxfp4: rstd
-  float R;     // nvfp4
+  float mul;   // E4M3: codes are E4M3(value * mul); nvfp4: 2688 / R; mxfp4: rstd
+  float sf;    // nvfp4: block scales are E4M3(amax * sf), sf = 448 / R
 };
 
 // amax of the row's values (z for the norm) and rstd (1 but for the norm) to
@@ -147,7 +159,7 @@ __device__ __forceinline__ RowScale row_scale(float amax, float rstd, float &sca
   RowScale r;
   r.pre = amax < 0x1p-64f ? 0x1p64f : 1.0f;
   r.mul = rstd;
-  r.R = 0.0f;
+  r.sf = 0.0f;
   if constexpr (OUT == kOutE4M3) {
     const float s = __fdiv_rn(amax * rstd, 448.0f);
     scale = amax * rstd == 0.0f ? 1.0f : fmaxf(s, 0x1p-126f);
@@ -155,7 +167,9 @@ __device__ __forceinline__ RowScale row_scale(float amax, float rstd, float &sca
   } else if constexpr (OUT == kOutNvfp4) {
     const float top = amax * rstd;
     scale = top == 0.0f ? 1.0f : top >= kRowFloor ? __fdiv_rn(top, 2688.0f) : 0x1p-100f;
-    r.R = top >= kRowFloor ? amax * r.pre : rstd > 0.0f ? __fdiv_rn(kRowFloor, rstd) * r.pre : 1.0f;
+    const float R = top >= kRowFloor ? amax * r.pre : rstd > 0.0f ? __fdiv_rn(kRowFloor, rstd) * r.pre : 1.0f;
+    r.sf = __fdiv_rn(448.0f, R);
+    r.mul = 6.0f * r.sf;
   } else {
     r.pre = 1.0f;
   }
@@ -167,8 +181,9 @@ __device__ __forceinline__ RowScale row_scale(float amax, float rstd, float &sca
 // plain, 16 for z) a quotient is either on a rounding boundary of the code or
 // well away from it (2^-14 and 2^-20 relative), and the computed quotient,
 // within 2^-22, is moved onto the boundary by rounding it to 17 (22) bits: ties
-// are then decided as for the exact quotient.  (For nvfp4 behind the norm the
-// distance is 2^-22 only, so a tie's neighbour may be taken for one.)
+// are then decided as for the exact quotient.  (A code of nvfp4 behind the norm
+// is a quotient with 20 bits below the line, as close as 2^-22 to a boundary,
+// and computed to 2^-21.5: there most ties are decided so, not all.)
 template <int SRC>
 __device__ __forceinline__ float settle(float v) {
   if constexpr (SRC == kSrcGate) return v;
@@ -192,11 +207,8 @@ __device__ __forceinline__ void encode_chunk(const RowQuantArgs &p, int64_t row,
     if constexpr (OUT == kOutNvfp4) {
       float top = max_abs8(y);
       top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      // 0.875 top, sf / 512 * R and their quotients stay in range for every
-      // finite row; products with these constants are exact for bf16 values
-      code = e4m3_code(__fdiv_rn(0.875f * top, r.R) * 512.0f);
-      const float d = e4m3_value(code) * 0x1p-9f * r.R;
-      mul = code == 0u ? 0.0f : 5.25f * __frcp_rn(d);
+      code = e4m3_code(settle<SRC>(top * r.sf));
+      mul = code == 0u ? 0.0f : r.mul * rcp_approx(e4m3_value(code));
     } else {
       if constexpr (SRC == kSrcNorm) {
 #pragma unroll
@@ -230,14 +242,19 @@ __device__ __forceinline__ void flag(const RowQuantArgs &p) {
 }
 
 // NC: chunks a thread holds in registers; 0: the row is read twice.
-// WARP: a warp per row, else a CTA.
+// WARP: a warp per row, else a CTA, or `segs` CTAs where nothing is summed or
+// compared over the row.
 template <int SRC, int OUT, int NC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(const RowQuantArgs p) {
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(const RowQuantArgs p, int segs) {
   constexpr int kLive = NC > 0 ? NC : 1;
   __shared__ float2 red[32];
   const int threads = WARP ? 32 : static_cast<int>(blockDim.x);
-  const int t = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
-  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : static_cast<int64_t>(blockIdx.x);
+  constexpr bool kNeedMax = OUT != kOutMxfp4, kNeedSum = SRC == kSrcNorm, kSegs = !WARP && NC > 0 && !kNeedMax && !kNeedSum;
+  const int seg = kSegs ? static_cast<int>(blockIdx.x % segs) : 0;
+  const int t = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x) + seg * NC * threads;
+  const int64_t row = WARP    ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5)
+                      : kSegs ? static_cast<int64_t>(blockIdx.x / segs)
+                              : static_cast<int64_t>(blockIdx.x);
   const int chunks = static_cast<int>(p.cols / kChunk);
   const int64_t tiles = OUT == kOutNvfp4 ? (p.cols + 63) / 64 : (p.cols + 127) / 128;
   grid_dependency_wait();
@@ -245,16 +262,15 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
   if (row >= p.rows) {
     // a row past the matrix in its last band of 128: zero scales
     if (OUT != kOutE4M3 && row < (p.rows + 127) / 128 * 128)
-      for (int64_t i = t; i < tiles; i += threads)
+      for (int64_t i = threadIdx.x % threads + seg * threads; i < tiles; i += threads * segs)
         *reinterpret_cast<uint32_t *>(p.blocks + block_scale_offset(row, 4 * i, tiles)) = 0u;
     return;
   }
   // ---- first pass: values, sum of squares, largest magnitude
   float y[kLive][kChunk], sum = 0.0f, amax = 0.0f;
-  constexpr bool kNeedMax = OUT != kOutMxfp4, kNeedSum = SRC == kSrcNorm;
   auto take = [&](int c, float *v) {
     chunk_values<SRC>(p, row, c, true, v, sum);
-    if constexpr (kNeedMax) amax = max_nan(amax, max_abs8(v));
+    if constexpr (kNeedMax) amax = max_abs8(v, amax);
   };
   if constexpr (NC > 0) {
 #pragma unroll
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
         for (int k = 0; k < kChunk; ++k) y[i][k] = 0.0f;
       }
     }
-  } else if constexpr (kNeedMax || kNeedSum) {
+  } else {
 #pragma unroll 2
     for (int c = t; c < chunks; c += threads) take(c, y[0]);
   }
@@ -310,8 +326,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
     for (int c0 = t & ~31; c0 < chunks; c0 += threads) {
       const int c = c0 + (t & 31);
       float v[kChunk] = {}, none = 0.0f;
-      // (mxfp4 of plain or gated values has no first pass)
-      if (c < chunks) chunk_values<SRC>(p, row, c, !(kNeedMax || kNeedSum), v, none);
+      if (c < chunks) chunk_values<SRC>(p, row, c, false, v, none);
       put(c, c < chunks, v);
     }
   }
@@ -332,8 +347,8 @@ cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned th
 }
 
 template <int SRC, int OUT, int NC, bool WARP>
-cudaError_t launch_form(const RowQuantArgs &a, unsigned grid, unsigned threads, cudaStream_t st) {
-  return launch_dependent(rowquant_kernel<SRC, OUT, NC, WARP>, grid, threads, st, a);
+cudaError_t launch_form(const RowQuantArgs &a, unsigned grid, unsigned threads, cudaStream_t st, int segs = 1) {
+  return launch_dependent(rowquant_kernel<SRC, OUT, NC, WARP>, grid, threads, st, a, segs);
 }
 
 template <int SRC, int OUT>
@@ -346,14 +361,22 @@ cudaError_t launch_out(const RowQuantArgs &a, cudaStream_t st) {
     return launch_form<SRC, OUT, 4, true>(a, grid, 32 * kWarpRows, st);
   }
   const unsigned grid = static_cast<unsigned>(rows);
-  if (chunks > 4 * 1024) return launch_form<SRC, OUT, 0, false>(a, grid, 1024, st);
-  // few rows: as many threads on each as there are chunks; many: four (two)
-  // chunks a thread, for more loads in flight
-  const int nc = chunks <= 1024 && a.rows <= kFewRows ? 1 : chunks <= 2048 && a.rows <= kFewRows ? 2 : 4;
-  const unsigned threads = static_cast<unsigned>((chunks + 32 * nc - 1) / (32 * nc) * 32);
-  if (nc == 1) return launch_form<SRC, OUT, 1, false>(a, grid, threads, st);
-  if (nc == 2) return launch_form<SRC, OUT, 2, false>(a, grid, threads, st);
-  return launch_form<SRC, OUT, 4, false>(a, grid, threads, st);
+  if constexpr (OUT == kOutMxfp4 && SRC != kSrcNorm) {
+    // nothing to reduce over the row: CTAs of up to 256 threads, two chunks
+    // each (rows of over 1024 columns: far fewer CTAs than a grid may have)
+    const int64_t segs = (chunks + 511) / 512;
+    const unsigned threads = static_cast<unsigned>((chunks + 64 * segs - 1) / (64 * segs) * 32);
+    return launch_form<SRC, OUT, 2, false>(a, static_cast<unsigned>(segs * rows), threads, st, static_cast<int>(segs));
+  } else {
+    if (chunks > 4 * 1024) return launch_form<SRC, OUT, 0, false>(a, grid, 1024, st);
+    // few rows: as many threads on each as there are chunks; many: four (two)
+    // chunks a thread, for more loads in flight
+    const int nc = chunks <= 1024 && a.rows <= kFewRows ? 1 : chunks <= 2048 && a.rows <= kFewRows ? 2 : 4;
+    const unsigned threads = static_cast<unsigned>((chunks + 32 * nc - 1) / (32 * nc) * 32);
+    if (nc == 1) return launch_form<SRC, OUT, 1, false>(a, grid, threads, st);
+    if (nc == 2) return launch_form<SRC, OUT, 2, false>(a, grid, threads, st);
+    return launch_form<SRC, OUT, 4, false>(a, grid, threads, st);
+  }
 }
 
 template <int SRC>
