@@ -424,7 +424,8 @@ int sp24_gemm_packed_scaled(const void *Xq, const float *x_scales, int x_per_tok
 /*
  * Block-scaled FP4 (beyond the pages, whose FP4 has one scale per tensor; the
  * SlideSparse summary names the precision, §3 "Contribuciones Clave").  Codes
- * are E2M1 as above, two per byte, element 2i in the low nibble of byte i.
+ * are E2M1 as above, two per byte, element 2i in the low nibble of byte i (a
+ * zero may carry either sign).
  * Two formats:
  *   SP24_FP4_NVFP4: per row R = max(amax, 2688 * 2^-100) and row_scale =
  *     RN(R / 2688) (1 for an all-zero row); per block of 16 along the row sf =

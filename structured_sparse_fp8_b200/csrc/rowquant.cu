@@ -31,6 +31,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "micro_common.cuh"
 #include "micro_kernels.h"
 #include "quant_common.cuh"
@@ -46,7 +48,8 @@ enum RowSrc : int { kSrcPlain = 0, kSrcNorm = 1, kSrcGate = 2 };
 constexpr int kChunk = 8;                    // elements per thread and load
 constexpr int kWarpRows = 8;                 // rows of a CTA in the warp-per-row form
 constexpr float kRowFloor = 0x1.5p-89f;      // 2688 * 2^-100
-constexpr int64_t kFewRows = 296;             // two CTAs an SM
+constexpr int64_t kFewRows = 2 * 148;         // two CTAs an SM
+constexpr int64_t kStreamRows = 8 * 148, kStreamChunks = 768;  // what the streamed form starts from
 constexpr float kInf = __builtin_huge_valf();
 
 // ld.global (not .nc: residual_out may be x or residual), kept out of L1
@@ -57,13 +60,53 @@ __device__ __forceinline__ uint4 ld_row(const uint16_t *p) {
                : "l"(p));
   return v;
 }
-__device__ __forceinline__ void unpack8(const uint4 &a, float *v) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+
+// Two fp32 values in a register pair, and the packed operations on them: such
+// stages are bound by instruction issue next to memory, and these halve it.
+typedef uint64_t f2;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
+
+// 8 values of a chunk.
+struct Chunk {
+  f2 v[4];
+  __device__ __forceinline__ void scale(float m) {
+    const f2 mm = both(m);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], mm);
   }
+};
+
+__device__ __forceinline__ Chunk unpack8(const uint4 &a) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  Chunk c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c.v[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return c;
 }
 
 // NaN wins, so that one in a row is seen in its largest value
@@ -83,7 +126,7 @@ __device__ __forceinline__ float warp_max(float v) {
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-// 1 / v to one step, v a normal number
+// 1 / v to one step; results below 2^-126 are 0
 __device__ __forceinline__ float rcp_approx(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -95,145 +138,214 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 // The largest of `so_far` (>= 0) and the chunk's magnitudes.
-__device__ __forceinline__ float max_abs8(const float *y, float so_far = 0.0f) {
+__device__ __forceinline__ float max_abs8(const Chunk &c, float so_far = 0.0f) {
 #pragma unroll
-  for (int i = 0; i < kChunk; i += 2) so_far = max_abs3(so_far, y[i], y[i + 1]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = split2(c.v[i]);
+    so_far = max_abs3(so_far, v.x, v.y);
+  }
   return so_far;
+}
+
+// bf16(x + r) of 8 values: the sum of two bf16 values rounded once (fp32 holds
+// every such sum that is near a rounding boundary exactly)
+__device__ __forceinline__ uint4 add_bf16(const uint4 &x, const uint4 &r) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {r.x, r.y, r.z, r.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&a[i]), *reinterpret_cast<const __nv_bfloat162 *>(&b[i]));
+    o[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// z = h * w, and the sum of h^2
+__device__ __forceinline__ Chunk norm_values(const uint4 &h, const uint4 &w, f2 &sum) {
+  Chunk y = unpack8(h);
+  const Chunk ww = unpack8(w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum = fma2(y.v[i], y.v[i], sum);
+    y.v[i] = mul2(y.v[i], ww.v[i]);
+  }
+  return y;
+}
+
+// g / (1 + exp(-g)) * u.  Where exp(-g) leaves fp32's range its reciprocal is 0.
+__device__ __forceinline__ Chunk gate_values(const uint4 &gv, const uint4 &uv) {
+  Chunk g = unpack8(gv);
+  const Chunk u = unpack8(uv);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = split2(mul2(g.v[i], both(-1.4426950408889634f)));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(a.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(a.y));
+    const float2 d = split2(add2(pack2(e.x, e.y), both(1.0f)));
+    g.v[i] = mul2(mul2(g.v[i], pack2(rcp_approx(d.x), rcp_approx(d.y))), u.v[i]);
+  }
+  return g;
+}
+
+// A row's pointers (64-bit products once per row; offsets within it are 32-bit).
+struct Row {
+  const uint16_t *x, *residual;  // of the gated form: gate, up
+  uint16_t *h;                   // the norm's sum, written and read back
+  uint8_t *q, *blocks;           // blocks: scale 0 of the row; tile i is 512 i bytes on
+};
+template <int SRC, int OUT>
+__device__ __forceinline__ Row row_of(const RowQuantArgs &p, int64_t row, int tiles) {
+  Row r;
+  r.x = p.x + row * p.cols * (SRC == kSrcGate ? 2 : 1);
+  r.residual = SRC == kSrcGate ? r.x + p.cols : p.residual ? p.residual + row * p.cols : nullptr;
+  r.h = p.residual_out + row * p.cols;
+  r.q = p.q + row * (OUT == kOutE4M3 ? p.cols : p.cols / 2);
+  r.blocks = p.blocks + block_scale_offset(row, 0, tiles);
+  return r;
 }
 
 // What chunk `c` of the row contributes: y, or z = h * w for the norm (then
 // also its sum of squares; `first` adds the residual and stores h).
 template <int SRC>
-__device__ __forceinline__ void chunk_values(const RowQuantArgs &p, int64_t row, int c, bool first, float *y, float &sum) {
-  const int64_t at = row * p.cols + static_cast<int64_t>(c) * kChunk;
+__device__ __forceinline__ Chunk chunk_values(const RowQuantArgs &p, const Row &row, int c, bool first, f2 &sum) {
+  const int at = c * kChunk;
   if constexpr (SRC == kSrcPlain) {
-    unpack8(ld_row(p.x + at), y);
+    return unpack8(ld_row(row.x + at));
   } else if constexpr (SRC == kSrcNorm) {
-    float w[kChunk];
-    const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(p.weight) + c);
+    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.weight) + c);
+    uint4 h;
     if (first && p.residual) {
-      const uint4 xv = ld_row(p.x + at), rv = ld_row(p.residual + at);
-      float r[kChunk];
-      unpack8(xv, y);
-      unpack8(rv, r);
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h2 = __floats2bfloat162_rn(y[2 * i] + r[2 * i], y[2 * i + 1] + r[2 * i + 1]);
-        o[i] = *reinterpret_cast<const uint32_t *>(&h2);
-      }
-      const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4 *>(p.residual_out + at) = ov;
-      unpack8(ov, y);
+      const uint4 x = ld_row(row.x + at), r = ld_row(row.residual + at);
+      h = add_bf16(x, r);
+      *reinterpret_cast<uint4 *>(row.h + at) = h;
     } else {
-      unpack8(ld_row((p.residual ? p.residual_out : p.x) + at), y);
+      h = ld_row((p.residual ? row.h : row.x) + at);
     }
-    unpack8(wv, w);
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      if (first) sum = fmaf(y[i], y[i], sum);
-      y[i] *= w[i];
-    }
+    return norm_values(h, w, sum);
   } else {
-    const int64_t g = row * 2 * p.cols + static_cast<int64_t>(c) * kChunk;
-    float u[kChunk];
-    const uint4 gv = ld_row(p.x + g), uv = ld_row(p.x + g + p.cols);
-    unpack8(gv, y);
-    unpack8(uv, u);
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) y[i] = __fdividef(y[i], 1.0f + __expf(-y[i])) * u[i];
+    const uint4 g = ld_row(row.x + at), u = ld_row(row.residual + at);
+    return gate_values(g, u);
   }
 }
 
-// How a row's values become codes: one factor for the row (E4M3), or R.
+// How a row's values become codes.  Every thread works these out, so they are
+// made with a refined reciprocal (within 2^-23) and not by division.
 struct RowScale {
   float pre;   // factor for values of a row so small that its quotients would leave fp32's range, else 1
   float mul;   // E4M3: codes are E4M3(value * mul); nvfp4: 2688 / R; mxfp4: rstd
   float sf;    // nvfp4: block scales are E4M3(amax * sf), sf = 448 / R
 };
+__device__ __forceinline__ float rcp_refined(float v) {
+  const float r = rcp_approx(v);
+  return fmaf(r, fmaf(-v, r, 1.0f), r);
+}
 
-// amax of the row's values (z for the norm) and rstd (1 but for the norm) to
-// the row's scale and factors.
+// From amax of the row's values (z for the norm) and rstd (1 but for the norm).
 template <int OUT>
-__device__ __forceinline__ RowScale row_scale(float amax, float rstd, float &scale) {
+__device__ __forceinline__ RowScale row_scale(float amax, float rstd) {
   RowScale r;
-  r.pre = amax < 0x1p-64f ? 0x1p64f : 1.0f;
+  r.pre = 1.0f;
   r.mul = rstd;
   r.sf = 0.0f;
-  if constexpr (OUT == kOutE4M3) {
-    const float s = __fdiv_rn(amax * rstd, 448.0f);
-    scale = amax * rstd == 0.0f ? 1.0f : fmaxf(s, 0x1p-126f);
-    r.mul = amax == 0.0f ? 0.0f : s >= 0x1p-126f ? __fdiv_rn(448.0f, amax * r.pre) : __fdiv_rn(rstd, scale) * (1.0f / r.pre);
-  } else if constexpr (OUT == kOutNvfp4) {
-    const float top = amax * rstd;
-    scale = top == 0.0f ? 1.0f : top >= kRowFloor ? __fdiv_rn(top, 2688.0f) : 0x1p-100f;
-    const float R = top >= kRowFloor ? amax * r.pre : rstd > 0.0f ? __fdiv_rn(kRowFloor, rstd) * r.pre : 1.0f;
-    r.sf = __fdiv_rn(448.0f, R);
-    r.mul = 6.0f * r.sf;
-  } else {
-    r.pre = 1.0f;
+  if constexpr (OUT != kOutMxfp4) {
+    // a row of ordinary size: its own amax decides
+    const float least = OUT == kOutE4M3 ? 448.0f * 0x1p-126f : kRowFloor;
+    if (amax >= 0x1p-64f && amax <= 0x1p100f && amax * rstd >= least) {
+      r.sf = 448.0f * rcp_refined(amax);
+    } else {
+      const float big = amax > 0x1p100f ? 0x1p-64f : 0x1p64f;
+      r.pre = big;
+      // (the row's values are multiplied by pre first)
+      const float R = amax * rstd >= least ? amax * big : rstd > 0.0f ? __fdiv_rn(least, rstd) * big : 1.0f;
+      r.sf = __fdiv_rn(448.0f, R);
+    }
+    r.mul = OUT == kOutE4M3 ? r.sf : 6.0f * r.sf;
   }
   return r;
 }
-
-// Bits dropped (rounded) from a quotient of two of the row's values before it
-// is rounded to a code.  Where the values have few significant bits (8 for
-// plain, 16 for z) a quotient is either on a rounding boundary of the code or
-// well away from it (2^-14 and 2^-20 relative), and the computed quotient,
-// within 2^-22, is moved onto the boundary by rounding it to 17 (22) bits: ties
-// are then decided as for the exact quotient.  (A code of nvfp4 behind the norm
-// is a quotient with 20 bits below the line, as close as 2^-22 to a boundary,
-// and computed to 2^-21.5: there most ties are decided so, not all.)
-template <int SRC>
-__device__ __forceinline__ float settle(float v) {
-  if constexpr (SRC == kSrcGate) return v;
-  constexpr uint32_t drop = SRC == kSrcPlain ? 7 : 2;
-  return __uint_as_float((__float_as_uint(v) + (1u << (drop - 1))) & ~((1u << drop) - 1));
+// The row's stored scale.
+template <int OUT>
+__device__ __forceinline__ float stored_scale(float top) {  // top = amax * rstd
+  if (OUT == kOutE4M3) return top == 0.0f ? 1.0f : fmaxf(__fdiv_rn(top, 448.0f), 0x1p-126f);
+  return top == 0.0f ? 1.0f : top >= kRowFloor ? __fdiv_rn(top, 2688.0f) : 0x1p-100f;
 }
 
-// Codes of one chunk, and its block's scale.  Every lane of the warp takes
-// part; `on` lanes store.
+// Quotients of two of the row's values that are to be rounded to a code, where
+// the values have few significant bits, are either on a rounding boundary of
+// the code or well away from it; computed to 2^-21.5 of themselves, they are
+// first rounded to fewer bits, which moves them onto the boundary, so that ties
+// are decided as for the exact quotient.
+// Block scales, 448 amax_b / R: 17 bits for plain values (at least 2^-13 from a
+// boundary otherwise), 22 for the norm's z (16 bits; 2^-20).
+template <int SRC>
+__device__ __forceinline__ float settle_scale(float v) {
+  constexpr int drop = SRC == kSrcPlain ? 7 : SRC == kSrcNorm ? 2 : 0;
+  return __uint_as_float((__float_as_uint(v) + ((1u << drop) >> 1)) & ~((1u << drop) - 1));
+}
+// Codes of plain values, 2688 x / (sf R), below 8: the boundaries are multiples
+// of 1/4, other quotients at least 2^-13.9 from them (15 * 255 below the line);
+// adding and subtracting 768 rounds to a multiple of 2^-14.
+constexpr float kSettle = 768.0f;
+
+// The E4M3 code of a value that is not negative.
+__device__ __forceinline__ uint32_t e4m3_code_positive(float v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
+  return r;
+}
+
+// Codes of one chunk whose largest magnitude is `top`, and its block's scale.
+// Every lane of the warp takes part; `on` lanes store.
 template <int SRC, int OUT>
-__device__ __forceinline__ void encode_chunk(const RowQuantArgs &p, int64_t row, int c, bool on, const RowScale &r, float *y,
-                                             int64_t tiles) {
+__device__ __forceinline__ void encode_chunk(const RowQuantArgs &p, const Row &row, int c, bool on, const RowScale &r, Chunk y,
+                                             float top) {
   const int lane = threadIdx.x & 31;
-  if constexpr (OUT == kOutE4M3) {
+  float v[kChunk];
+  auto spread = [&] {
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) y[i] = settle<SRC>(y[i] * r.mul);
-    if (on) *reinterpret_cast<uint2 *>(p.q + row * p.cols + static_cast<int64_t>(c) * kChunk) = make_uint2(e4m3_codes4(y), e4m3_codes4(y + 4));
+    for (int i = 0; i < 4; ++i) {
+      const float2 s = split2(y.v[i]);
+      v[2 * i] = s.x, v[2 * i + 1] = s.y;
+    }
+  };
+  if constexpr (OUT == kOutE4M3) {
+    y.scale(r.mul);
+    spread();
+    if (on) *reinterpret_cast<uint2 *>(row.q + c * kChunk) = make_uint2(e4m3_codes4(v), e4m3_codes4(v + 4));
   } else {
     float mul;
     uint32_t code;
     if constexpr (OUT == kOutNvfp4) {
-      float top = max_abs8(y);
       top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      code = e4m3_code(settle<SRC>(top * r.sf));
+      code = e4m3_code_positive(settle_scale<SRC>(top * r.sf));
       mul = code == 0u ? 0.0f : r.mul * rcp_approx(e4m3_value(code));
     } else {
       if constexpr (SRC == kSrcNorm) {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) y[i] *= r.mul;
+        top *= r.mul;
+        y.scale(r.mul);
       }
-      float top = max_abs8(y);
       top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       if (!(top < kInf) && p.status) atomicOr(p.status, SP24_STATUS_NONFINITE);
       code = static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(top) >> 23) - 2, 0));
       mul = __uint_as_float((254u - code) << 23);
     }
+    if constexpr (OUT == kOutNvfp4 && SRC == kSrcPlain) {
+      const f2 m = both(mul), up = both(kSettle), down = both(-kSettle);
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      y[i] *= mul;
-      if constexpr (OUT == kOutNvfp4) y[i] = settle<SRC>(y[i]);
+      for (int i = 0; i < 4; ++i) y.v[i] = add2(fma2(y.v[i], m, up), down);
+    } else {
+      y.scale(mul);
     }
-    if (on) *reinterpret_cast<uint32_t *>(p.q + row * (p.cols / 2) + static_cast<int64_t>(c) * 4) = e2m1_codes8(y);
+    spread();
+    if (on) *reinterpret_cast<uint32_t *>(row.q + c * 4) = e2m1_codes8(v);
     // four block scales to a word (absent blocks of a last tile are zero)
     constexpr int lanes = OUT == kOutNvfp4 ? 2 : 4;  // per block
     uint32_t word = on ? code << (8 * (lane / lanes & 3)) : 0u;
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, lanes);
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * lanes);
-    if (on && lane % (4 * lanes) == 0)
-      *reinterpret_cast<uint32_t *>(p.blocks + block_scale_offset(row, c / lanes, tiles)) = word;
+    if (on && lane % (4 * lanes) == 0) *reinterpret_cast<uint32_t *>(row.blocks + c / (4 * lanes) * 512) = word;
   }
 }
 
@@ -242,53 +354,52 @@ __device__ __forceinline__ void flag(const RowQuantArgs &p) {
 }
 
 // NC: chunks a thread holds in registers; 0: the row is read twice.
-// WARP: a warp per row, else a CTA, or `segs` CTAs where nothing is summed or
-// compared over the row.
+// WARP: a warp per row, else a CTA, or gridDim.y CTAs where nothing is summed
+// or compared over the row.
 template <int SRC, int OUT, int NC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(const RowQuantArgs p, int segs) {
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(const RowQuantArgs p) {
   constexpr int kLive = NC > 0 ? NC : 1;
   __shared__ float2 red[32];
-  const int threads = WARP ? 32 : static_cast<int>(blockDim.x);
   constexpr bool kNeedMax = OUT != kOutMxfp4, kNeedSum = SRC == kSrcNorm, kSegs = !WARP && NC > 0 && !kNeedMax && !kNeedSum;
-  const int seg = kSegs ? static_cast<int>(blockIdx.x % segs) : 0;
+  const int threads = WARP ? 32 : static_cast<int>(blockDim.x);
+  const int seg = kSegs ? static_cast<int>(blockIdx.y) : 0, segs = kSegs ? static_cast<int>(gridDim.y) : 1;
   const int t = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x) + seg * NC * threads;
-  const int64_t row = WARP    ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5)
-                      : kSegs ? static_cast<int64_t>(blockIdx.x / segs)
-                              : static_cast<int64_t>(blockIdx.x);
+  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : static_cast<int64_t>(blockIdx.x);
   const int chunks = static_cast<int>(p.cols / kChunk);
-  const int64_t tiles = OUT == kOutNvfp4 ? (p.cols + 63) / 64 : (p.cols + 127) / 128;
+  const int tiles = static_cast<int>(OUT == kOutNvfp4 ? (p.cols + 63) / 64 : (p.cols + 127) / 128);
   grid_dependency_wait();
   grid_launch_dependents();
   if (row >= p.rows) {
     // a row past the matrix in its last band of 128: zero scales
     if (OUT != kOutE4M3 && row < (p.rows + 127) / 128 * 128)
-      for (int64_t i = threadIdx.x % threads + seg * threads; i < tiles; i += threads * segs)
-        *reinterpret_cast<uint32_t *>(p.blocks + block_scale_offset(row, 4 * i, tiles)) = 0u;
+      for (int i = threadIdx.x % threads + seg * threads; i < tiles; i += threads * segs)
+        *reinterpret_cast<uint32_t *>(p.blocks + block_scale_offset(row, 4 * static_cast<int64_t>(i), tiles)) = 0u;
     return;
   }
   // ---- first pass: values, sum of squares, largest magnitude
-  float y[kLive][kChunk], sum = 0.0f, amax = 0.0f;
-  auto take = [&](int c, float *v) {
-    chunk_values<SRC>(p, row, c, true, v, sum);
-    if constexpr (kNeedMax) amax = max_abs8(v, amax);
+  const Row at = row_of<SRC, OUT>(p, row, tiles);
+  Chunk y[kLive];
+  f2 sums = 0;
+  float top[kLive], sum = 0.0f, amax = 0.0f;
+  auto take = [&](int c, Chunk &v, float &most) {
+    v = chunk_values<SRC>(p, at, c, true, sums);
+    most = max_abs8(v);
+    if constexpr (kNeedMax) amax = max_nan(amax, most);
   };
   if constexpr (NC > 0) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      if (t + i * threads < chunks) {
-        take(t + i * threads, y[i]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kChunk; ++k) y[i][k] = 0.0f;
-      }
+      y[i] = Chunk{};
+      top[i] = 0.0f;
+      if (t + i * threads < chunks) take(t + i * threads, y[i], top[i]);
     }
   } else {
 #pragma unroll 2
-    for (int c = t; c < chunks; c += threads) take(c, y[0]);
+    for (int c = t; c < chunks; c += threads) take(c, y[0], top[0]);
   }
   if constexpr (kNeedMax || kNeedSum) {
     if constexpr (kNeedMax) amax = warp_max(amax);
-    if constexpr (kNeedSum) sum = warp_sum(sum);
+    if constexpr (kNeedSum) sum = warp_sum(split2(sums).x + split2(sums).y);
     if constexpr (!WARP) {
       const int warps = threads >> 5, lane = t & 31;
       if (lane == 0) red[t >> 5] = make_float2(amax, sum);
@@ -303,40 +414,186 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
     const float ms = __fdiv_rn(sum, static_cast<float>(p.cols)) + p.eps;
     rstd = ms > 0.0f ? __frsqrt_rn(ms) : 0.0f;
   }
-  float scale = 1.0f;
-  const RowScale r = row_scale<OUT>(amax, rstd, scale);
+  const RowScale r = row_scale<OUT>(amax, rstd);
   if (t == 0) {
-    if constexpr (kNeedMax) p.scales[row] = scale;
+    if constexpr (kNeedMax) p.scales[row] = stored_scale<OUT>(amax * rstd);
     if ((kNeedMax && !(amax * rstd < kInf)) || (kNeedSum && !(sum < kInf))) flag(p);
   }
   // ---- second pass: codes
-  auto put = [&](int c, bool on, float *v) {
+  auto put = [&](int c, bool on, Chunk v, float most) {
     if (r.pre != 1.0f) {
-#pragma unroll
-      for (int k = 0; k < kChunk; ++k) v[k] *= r.pre;
+      most *= r.pre;
+      v.scale(r.pre);
     }
-    encode_chunk<SRC, OUT>(p, row, c, on, r, v, tiles);
+    encode_chunk<SRC, OUT>(p, at, c, on, r, v, most);
   };
   if constexpr (NC > 0) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) put(t + i * threads, t + i * threads < chunks, y[i]);
+    for (int i = 0; i < NC; ++i) put(t + i * threads, t + i * threads < chunks, y[i], top[i]);
   } else {
     // a warp's lanes stay together: they share blocks
 #pragma unroll 2
     for (int c0 = t & ~31; c0 < chunks; c0 += threads) {
       const int c = c0 + (t & 31);
-      float v[kChunk] = {}, none = 0.0f;
-      if (c < chunks) chunk_values<SRC>(p, row, c, false, v, none);
-      put(c, c < chunks, v);
+      Chunk v{};
+      f2 none = 0;
+      if (c < chunks) v = chunk_values<SRC>(p, at, c, false, none);
+      put(c, c < chunks, v, max_abs8(v));
     }
   }
 }
 
+// Many rows: CTAs stay and take rows blockIdx.x, blockIdx.x + gridDim.x, ...,
+// whose inputs bulk copies bring into a ring of `depth` rows in shared memory
+// ahead of time, so that loads never wait for a row's arithmetic, and a
+// thread's offsets are worked out once.  Between the passes a row's values
+// stay in its place in the ring: as fp32 where two bf16 inputs made room
+// (norm with a residual, gate), else as they came.
+struct StreamShape {
+  int depth;
+  uint32_t stage;   // bytes of a row's inputs
+};
+constexpr uint32_t kStreamBars = 128;  // barriers and their padding in front of the ring
+
+template <int SRC, int OUT, int T>
+__global__ void __launch_bounds__(T, 1024 / T) stream_row_kernel(const RowQuantArgs p, const StreamShape shape) {
+  constexpr bool kNeedMax = OUT != kOutMxfp4, kNeedSum = SRC == kSrcNorm;
+  constexpr int kWarps = T / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 red[2][kWarps];
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem);
+  uint8_t *ring = smem + kStreamBars;
+  const uint4 *weight = reinterpret_cast<const uint4 *>(ring + shape.depth * shape.stage);
+  const int t = static_cast<int>(threadIdx.x), lane = t & 31;
+  const int chunks = static_cast<int>(p.cols / kChunk);
+  const int tiles = static_cast<int>(OUT == kOutNvfp4 ? (p.cols + 63) / 64 : (p.cols + 127) / 128);
+  const uint32_t half = static_cast<uint32_t>(p.cols) * 2;  // bytes of one bf16 row
+  const bool two = SRC == kSrcGate || (SRC == kSrcNorm && p.residual);
+  const uint64_t policy = l2_policy_evict_first();
+  auto load = [&](int64_t row, int s) {
+    mbar_arrive_expect_tx(&full[s], shape.stage);
+    uint8_t *dst = ring + s * shape.stage;
+    if constexpr (SRC == kSrcGate) {
+      bulk_load_g2s(dst, p.x + row * 2 * p.cols, 2 * half, &full[s], policy);
+    } else {
+      bulk_load_g2s(dst, p.x + row * p.cols, half, &full[s], policy);
+      if (SRC == kSrcNorm && p.residual) bulk_load_g2s(dst + half, p.residual + row * p.cols, half, &full[s], policy);
+    }
+  };
+  if (t == 0) {
+    for (int s = 0; s < shape.depth; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t first = blockIdx.x, step = gridDim.x;
+  if (t == 0)
+    for (int s = 0; s < shape.depth; ++s)
+      if (first + s * step < p.rows) load(first + s * step, s);
+  if constexpr (SRC == kSrcNorm) {
+    for (int c = t; c < chunks; c += T) const_cast<uint4 *>(weight)[c] = __ldg(reinterpret_cast<const uint4 *>(p.weight) + c);
+    __syncthreads();
+  }
+  int s = 0;
+  uint32_t phase = 0;
+  for (int64_t row = first, i = 0; row < p.rows; row += step, ++i) {
+    const Row at = row_of<SRC, OUT>(p, row, tiles);
+    uint4 *in = reinterpret_cast<uint4 *>(ring + s * shape.stage);
+    uint4 *in2 = reinterpret_cast<uint4 *>(ring + s * shape.stage + half);
+    mbar_wait(&full[s], phase, p.status);
+    // the values of chunk c: first read, and read again
+    auto first_values = [&](int c, f2 &sums) {
+      if constexpr (SRC == kSrcPlain) {
+        return unpack8(in[c]);
+      } else if constexpr (SRC == kSrcGate) {
+        return gate_values(in[c], in2[c]);
+      } else {
+        uint4 h = in[c];
+        if (two) {
+          h = add_bf16(h, in2[c]);
+          *reinterpret_cast<uint4 *>(at.h + c * kChunk) = h;
+        }
+        return norm_values(h, weight[c], sums);
+      }
+    };
+    auto keep = [&](int c, const Chunk &y) {
+      if (two) {
+        in[c] = *reinterpret_cast<const uint4 *>(&y.v[0]);
+        in2[c] = *reinterpret_cast<const uint4 *>(&y.v[2]);
+      }
+    };
+    auto kept = [&](int c) {
+      Chunk y;
+      if (SRC != kSrcPlain && two) {
+        *reinterpret_cast<uint4 *>(&y.v[0]) = in[c];
+        *reinterpret_cast<uint4 *>(&y.v[2]) = in2[c];
+      } else if constexpr (SRC == kSrcNorm) {
+        f2 none = 0;
+        y = norm_values(in[c], weight[c], none);
+      } else {
+        y = unpack8(in[c]);
+      }
+      return y;
+    };
+    float rstd = 1.0f, amax = 0.0f;
+    if constexpr (kNeedMax || kNeedSum) {
+      float sum = 0.0f;
+      f2 sums = 0;
+#pragma unroll 2
+      for (int c = t; c < chunks; c += T) {
+        const Chunk y = first_values(c, sums);
+        if constexpr (kNeedMax) amax = max_abs8(y, amax);
+        if constexpr (SRC != kSrcPlain) keep(c, y);
+      }
+      if constexpr (kNeedMax) amax = warp_max(amax);
+      if constexpr (kNeedSum) sum = warp_sum(split2(sums).x + split2(sums).y);
+      if (lane == 0) red[i & 1][t >> 5] = make_float2(amax, sum);
+      __syncthreads();
+      const float2 v = lane < kWarps ? red[i & 1][lane] : make_float2(0.0f, 0.0f);
+      if constexpr (kNeedMax) amax = warp_max(v.x);
+      if constexpr (kNeedSum) {
+        sum = warp_sum(v.y);
+        const float ms = __fdiv_rn(sum, static_cast<float>(p.cols)) + p.eps;
+        rstd = ms > 0.0f ? __frsqrt_rn(ms) : 0.0f;
+      }
+      if (t == 0 && ((kNeedMax && !(amax * rstd < kInf)) || (kNeedSum && !(sum < kInf)))) flag(p);
+    }
+    const RowScale r = row_scale<OUT>(amax, rstd);
+    if (kNeedMax && t == 0) p.scales[row] = stored_scale<OUT>(amax * rstd);
+#pragma unroll 2
+    for (int c = t; c < (chunks + 31 & ~31); c += T) {  // a warp's lanes stay together
+      Chunk y{};
+      f2 none = 0;
+      if (c < chunks) {
+        if constexpr (kNeedMax || kNeedSum)
+          y = kept(c);
+        else
+          y = first_values(c, none);
+      }
+      if (r.pre != 1.0f) y.scale(r.pre);
+      encode_chunk<SRC, OUT>(p, at, c, c < chunks, r, y, max_abs8(y));
+    }
+    // the row's place in the ring is free: its next row
+    if constexpr (SRC != kSrcPlain && (kNeedMax || kNeedSum)) fence_proxy_async_smem();
+    __syncthreads();
+    if (t == 0 && row + shape.depth * step < p.rows) load(row + shape.depth * step, s);
+    if (++s == shape.depth) s = 0, phase ^= 1u;
+  }
+  // rows past the matrix in its last band of 128: zero scales
+  if constexpr (OUT != kOutE4M3)
+    for (int64_t row = p.rows + blockIdx.x; row < (p.rows + 127) / 128 * 128; row += step)
+      for (int k = t; k < tiles; k += T)
+        *reinterpret_cast<uint32_t *>(p.blocks + block_scale_offset(row, 4 * static_cast<int64_t>(k), tiles)) = 0u;
+}
+
 template <typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned threads, cudaStream_t st, Args... args) {
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, unsigned threads, uint32_t smem, cudaStream_t st,
+                             Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -347,10 +604,49 @@ cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned th
 }
 
 template <int SRC, int OUT, int NC, bool WARP>
-cudaError_t launch_form(const RowQuantArgs &a, unsigned grid, unsigned threads, cudaStream_t st, int segs = 1) {
-  return launch_dependent(rowquant_kernel<SRC, OUT, NC, WARP>, grid, threads, st, a, segs);
+cudaError_t launch_form(const RowQuantArgs &a, unsigned grid, unsigned threads, cudaStream_t st, unsigned segs = 1) {
+  return launch_dependent(rowquant_kernel<SRC, OUT, NC, WARP>, dim3(grid, segs, 1), threads, 0, st, a);
 }
 
+// The streamed form, where it has work for its CTAs and its rows fit; false
+// otherwise.
+template <int SRC, int OUT, int T>
+bool launch_stream(const RowQuantArgs &a, cudaStream_t st, cudaError_t &err) {
+  constexpr uint32_t kSm = 227 * 1024;
+  const uint64_t row = static_cast<uint64_t>(a.cols) * 2;
+  const uint64_t stage = row * (SRC == kSrcGate || a.residual ? 2 : 1), fixed = (SRC == kSrcNorm ? row : 0) + kStreamBars;
+  // CTAs an SM: as many as hold two rows each
+  uint64_t per = 1024 / T;
+  while (per > 1 && (2 * stage + fixed + 1280) * per > kSm) --per;
+  const uint64_t room = kSm / per - 1280;  // what the system and the reduction take of each
+  if (2 * stage + fixed > room) return false;
+  const uint64_t rounds = (a.rows + 148 * per - 1) / (148 * per);
+  uint64_t depth = (room - fixed) / stage;
+  depth = depth > 4 ? 4 : depth;
+  depth = depth > rounds ? rounds : depth;
+  const StreamShape sh{static_cast<int>(depth), static_cast<uint32_t>(stage)};
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(stream_row_kernel<SRC, OUT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024 - 512);
+  });
+  err = attr;
+  if (err != cudaSuccess) return true;
+  const int64_t most = static_cast<int64_t>(148 * per), grid = a.rows < most ? a.rows : most;
+  err = launch_dependent(stream_row_kernel<SRC, OUT, T>, dim3(static_cast<unsigned>(grid)), T,
+                         static_cast<uint32_t>(fixed + depth * stage), st, a, sh);
+  return true;
+}
+
+// Times in us at 4096 rows with cold inputs, the norm (residual) to E4M3 / the
+// gate to E4M3 / the plain quantiser to nvfp4:
+//   columns      a CTA a row, 2 or 4 chunks a thread    streamed
+//   4096         21.6 / 16.6 / 14.2 (2 chunks)          24.0 / 17.1 / 15.7
+//   8192         41.7 / 31.6 / 28.0 (2)                 43.0 / 29.8 / 22.5
+//   14336        84.8 / 68.1 / 58.6 (4)                 66.1 / 50.4 / 38.3
+// A wide row's CTA is so large that two or three fill an SM, and loads and
+// arithmetic no longer overlap.  Four chunks a thread at 4096 columns: 23.3 /
+// 19.1 / 16.5.
 template <int SRC, int OUT>
 cudaError_t launch_out(const RowQuantArgs &a, cudaStream_t st) {
   const int64_t rows = OUT == kOutE4M3 ? a.rows : (a.rows + 127) / 128 * 128;
@@ -363,15 +659,18 @@ cudaError_t launch_out(const RowQuantArgs &a, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(rows);
   if constexpr (OUT == kOutMxfp4 && SRC != kSrcNorm) {
     // nothing to reduce over the row: CTAs of up to 256 threads, two chunks
-    // each (rows of over 1024 columns: far fewer CTAs than a grid may have)
+    // each
     const int64_t segs = (chunks + 511) / 512;
     const unsigned threads = static_cast<unsigned>((chunks + 64 * segs - 1) / (64 * segs) * 32);
-    return launch_form<SRC, OUT, 2, false>(a, static_cast<unsigned>(segs * rows), threads, st, static_cast<int>(segs));
+    return launch_form<SRC, OUT, 2, false>(a, grid, threads, st, static_cast<unsigned>(segs));
   } else {
+    if (a.rows >= kStreamRows && chunks >= kStreamChunks) {
+      cudaError_t err;
+      if (chunks <= 1152 ? launch_stream<SRC, OUT, 256>(a, st, err) : launch_stream<SRC, OUT, 512>(a, st, err)) return err;
+    }
     if (chunks > 4 * 1024) return launch_form<SRC, OUT, 0, false>(a, grid, 1024, st);
-    // few rows: as many threads on each as there are chunks; many: four (two)
-    // chunks a thread, for more loads in flight
-    const int nc = chunks <= 1024 && a.rows <= kFewRows ? 1 : chunks <= 2048 && a.rows <= kFewRows ? 2 : 4;
+    // few rows: as many threads on each as there are chunks
+    const int nc = chunks <= 1024 && a.rows <= kFewRows ? 1 : chunks <= (a.rows <= kFewRows ? 2048 : 1024) ? 2 : 4;
     const unsigned threads = static_cast<unsigned>((chunks + 32 * nc - 1) / (32 * nc) * 32);
     if (nc == 1) return launch_form<SRC, OUT, 1, false>(a, grid, threads, st);
     if (nc == 2) return launch_form<SRC, OUT, 2, false>(a, grid, threads, st);
@@ -417,7 +716,7 @@ cudaError_t launch_rowquant_gate(RowOut out, const RowQuantArgs &a, cudaStream_t
 
 cudaError_t launch_fp4_unpack(const uint8_t *q, int64_t bytes, uint8_t *out, cudaStream_t st) {
   const int64_t want = (bytes / 8 + 255) / 256;
-  return launch_dependent(unpack_kernel, static_cast<unsigned>(want < 148 * 32 ? want : 148 * 32), 256u, st, q, bytes, out);
+  return launch_dependent(unpack_kernel, dim3(static_cast<unsigned>(want < 148 * 32 ? want : 148 * 32)), 256u, 0, st, q, bytes, out);
 }
 
 }  // namespace sp24
