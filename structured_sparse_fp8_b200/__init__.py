@@ -607,7 +607,6 @@ def fp8_gemm_dense(xq: torch.Tensor, x_scale, wq: torch.Tensor, w_scale,
 # once, and the stream is taken as a raw handle.
 _FP4 = {"nvfp4": (_lib.FP4_NVFP4, 16), "mxfp4": (_lib.FP4_MXFP4, 32)}
 _U8, _BF16, _F32 = torch.uint8, torch.bfloat16, torch.float32
-_empty = torch.empty
 
 
 def _fp4_format(format: str):
@@ -619,36 +618,40 @@ def _fp4_format(format: str):
 
 
 def _bf16_rows(t, name):
-    """(rows, columns, device) of a call's first operand."""
+    """(rows, columns, device index) of a call's first operand."""
     if t.dtype != _BF16 or t.dim() != 2:
         raise Sp24Error(f"{name} must be a 2-D bf16 tensor")
     if not t.is_cuda or not t.is_contiguous():
         raise Sp24Error("tensors must be contiguous CUDA tensors")
-    rows, cols = t.shape
-    return rows, cols, t.device
+    return t.size(0), t.size(1), t.get_device()
 
 
-def _operand(t, name, dtype, numel, device):
-    """An input or output of a call: the right type and size, contiguous, on the device of the call."""
+def _operand(t, name, dtype, numel, index):
+    """Pointer of an input or output of a call: the right type and size,
+    contiguous, on the call's device."""
     if t.dtype != dtype or t.numel() != numel:
         raise Sp24Error(f"{name} has the wrong shape or dtype")
-    if t.device != device or not t.is_contiguous():
-        raise Sp24Error(f"{name} must be contiguous and on {device}")
+    if not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+        raise Sp24Error(f"{name} must be contiguous and on cuda:{index}")
     return t.data_ptr()
 
 
-def _row_status(status, device):
-    return None if status is None else _operand(status, "status", torch.int32, 1, device)
+def _row_status(status, index):
+    return None if status is None else _operand(status, "status", torch.int32, 1, index)
 
 
-def _call(name, device, *args):
-    """One library call on `device`'s current stream, with that device current."""
-    fn = getattr(_lib.load(), name)
-    index = device.index
-    if index == torch.cuda.current_device():
+_functions: dict = {}
+
+
+def _call(name, index, *args):
+    """One library call on the device's current stream, with that device current."""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.load(), name)
+    if index == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc:
         _lib.check(rc, name)
@@ -663,7 +666,7 @@ def fp4_block_scales_size(rows: int, cols: int, format: str = "nvfp4") -> int:
     return _tiles_size(rows, cols, _fp4_format(format)[1])
 
 
-def _fp4_outputs(rows, cols, fmt, device, out):
+def _fp4_outputs(X, rows, cols, fmt, index, out):
     """(q, block_scales, row_scales) to write and their pointers: those of
     ``out``, new ones where it has none."""
     code, block = fmt
@@ -672,39 +675,39 @@ def _fp4_outputs(rows, cols, fmt, device, out):
     if out:
         q, blocks, scales = out.get("q"), out.get("block_scales"), out.get("row_scales")
     if q is None:
-        q = _empty((rows, cols // 2), dtype=_U8, device=device)
+        q = X.new_empty((rows, cols // 2), dtype=_U8)
         qp = q.data_ptr()
     else:
-        qp = _operand(q, "q", _U8, rows * (cols // 2), device)
+        qp = _operand(q, "q", _U8, rows * (cols // 2), index)
     if blocks is None:
-        blocks = _empty(size, dtype=_U8, device=device)
+        blocks = X.new_empty(size, dtype=_U8)
         bp = blocks.data_ptr()
     else:
-        bp = _operand(blocks, "block_scales", _U8, size, device)
+        bp = _operand(blocks, "block_scales", _U8, size, index)
     if code == _lib.FP4_MXFP4:
         return (q, blocks, None), qp, bp, None
     if scales is None:
-        scales = _empty(rows, dtype=_F32, device=device)
+        scales = X.new_empty(rows, dtype=_F32)
         sp = scales.data_ptr()
     else:
-        sp = _operand(scales, "row_scales", _F32, rows, device)
+        sp = _operand(scales, "row_scales", _F32, rows, index)
     return (q, blocks, scales), qp, bp, sp
 
 
-def _fp8_outputs(rows, cols, device, out):
+def _fp8_outputs(X, rows, cols, index, out):
     q = scales = None
     if out:
         q, scales = out.get("q"), out.get("scales")
     if q is None:
-        q = _empty((rows, cols), dtype=_U8, device=device)
+        q = X.new_empty((rows, cols), dtype=_U8)
         qp = q.data_ptr()
     else:
-        qp = _operand(q, "q", _U8, rows * cols, device)
+        qp = _operand(q, "q", _U8, rows * cols, index)
     if scales is None:
-        scales = _empty(rows, dtype=_F32, device=device)
+        scales = X.new_empty(rows, dtype=_F32)
         sp = scales.data_ptr()
     else:
-        sp = _operand(scales, "scales", _F32, rows, device)
+        sp = _operand(scales, "scales", _F32, rows, index)
     return q, scales, qp, sp
 
 
@@ -719,7 +722,7 @@ def fp4_quantize_microscaled(X: torch.Tensor, format: str = "nvfp4", status: tor
     """
     fmt = _fp4_format(format)
     rows, cols, dev = _bf16_rows(X, "X")
-    res, qp, bp, sp = _fp4_outputs(rows, cols, fmt, dev, out)
+    res, qp, bp, sp = _fp4_outputs(X, rows, cols, fmt, dev, out)
     _call("fp4_quantize_microscaled", dev, X.data_ptr(), rows, cols, fmt[0], qp, bp, sp, _row_status(status, dev))
     return res
 
@@ -729,25 +732,24 @@ def fp4_unpack_e4m3(q: torch.Tensor, out: torch.Tensor | None = None):
     if q.dtype != _U8 or q.dim() != 2:
         raise Sp24Error("q must be a 2-D uint8 tensor of packed FP4 codes")
     _require_cuda(q)
-    rows, half = q.shape
-    dev = q.device
+    rows, cols, dev = q.size(0), 2 * q.size(1), q.get_device()
     if out is None:
-        out = _empty((rows, 2 * half), dtype=_U8, device=dev)
+        out = q.new_empty((rows, cols))
         op = out.data_ptr()
     else:
-        op = _operand(out, "out", _U8, rows * 2 * half, dev)
-    _call("fp4_unpack_e4m3", dev, q.data_ptr(), rows, 2 * half, op)
+        op = _operand(out, "out", _U8, rows * cols, dev)
+    _call("fp4_unpack_e4m3", dev, q.data_ptr(), rows, cols, op)
     return out
 
 
-def _row_scales(t, name, count, device):
+def _row_scales(t, name, count, index):
     """(pointer, one per row) of a scale argument: None, one value, or one per row."""
     if t is None:
         return None, 0
     n = t.numel()
     if n != 1 and n != count:
         raise Sp24Error(f"{name} must hold one value or one per row")
-    return _operand(t, name, _F32, n, device), int(n != 1)
+    return _operand(t, name, _F32, n, index), int(n != 1)
 
 
 def fp4_gemm_microscaled(xq: torch.Tensor, x_block_scales: torch.Tensor, x_scales, wq: torch.Tensor,
@@ -760,15 +762,14 @@ def fp4_gemm_microscaled(xq: torch.Tensor, x_block_scales: torch.Tensor, x_scale
     if xq.dtype != _U8 or xq.dim() != 2 or wq.dim() != 2:
         raise Sp24Error("xq and wq must be 2-D uint8 tensors of packed FP4 codes")
     _require_cuda(xq)
-    m, half = xq.shape
-    n, dev = wq.shape[0], xq.device
+    m, half, n, dev = xq.size(0), xq.size(1), wq.size(0), xq.get_device()
     wp = _operand(wq, "wq", _U8, n * half, dev)
     xb = _operand(x_block_scales, "x_block_scales", _U8, _tiles_size(m, 2 * half, block), dev)
     wb = _operand(w_block_scales, "w_block_scales", _U8, _tiles_size(n, 2 * half, block), dev)
     xs, x_vec = _row_scales(x_scales, "x_scales", m, dev)
     ws, w_vec = _row_scales(w_scales, "w_scales", n, dev)
     if out is None:
-        out = _empty((m, n), dtype=_BF16, device=dev)
+        out = xq.new_empty((m, n), dtype=_BF16)
         yp = out.data_ptr()
     else:
         yp = _operand(out, "out", _BF16, m * n, dev)
@@ -801,7 +802,7 @@ def fp8_rmsnorm_quantize_pertoken(X: torch.Tensor, weight: torch.Tensor, eps: fl
     is X itself.  residual_out may be X or residual (in place); ``out`` may
     supply q and scales."""
     rows, cols, dev, wp, rp, hp, h = _norm_inputs(X, weight, residual, residual_out)
-    q, scales, qp, sp = _fp8_outputs(rows, cols, dev, out)
+    q, scales, qp, sp = _fp8_outputs(X, rows, cols, dev, out)
     _call("fp8_rmsnorm_quantize_pertoken", dev, X.data_ptr(), rp, wp, eps, rows, cols, hp, qp, sp,
           _row_status(status, dev))
     return q, scales, h
@@ -816,7 +817,7 @@ def fp4_rmsnorm_quantize_microscaled(X: torch.Tensor, weight: torch.Tensor, eps:
     fp4_quantize_microscaled, h as fp8_rmsnorm_quantize_pertoken."""
     fmt = _fp4_format(format)
     rows, cols, dev, wp, rp, hp, h = _norm_inputs(X, weight, residual, residual_out)
-    res, qp, bp, sp = _fp4_outputs(rows, cols, fmt, dev, out)
+    res, qp, bp, sp = _fp4_outputs(X, rows, cols, fmt, dev, out)
     _call("fp4_rmsnorm_quantize_microscaled", dev, X.data_ptr(), rp, wp, eps, rows, cols, fmt[0], hp, qp, bp, sp,
           _row_status(status, dev))
     return *res, h
@@ -833,7 +834,7 @@ def fp8_silu_mul_quantize_pertoken(GU: torch.Tensor, status: torch.Tensor | None
     """silu(gate) * up of GU bf16 [rows, 2 cols] (gate columns, then up columns)
     with E4M3 output: returns (q u8 [rows, cols], scales f32 [rows])."""
     rows, cols, dev = _gated_rows(GU)
-    q, scales, qp, sp = _fp8_outputs(rows, cols, dev, out)
+    q, scales, qp, sp = _fp8_outputs(GU, rows, cols, dev, out)
     _call("fp8_silu_mul_quantize_pertoken", dev, GU.data_ptr(), rows, cols, qp, sp, _row_status(status, dev))
     return q, scales
 
@@ -844,7 +845,7 @@ def fp4_silu_mul_quantize_microscaled(GU: torch.Tensor, format: str = "nvfp4", s
     returns (q, block_scales, row_scales) as fp4_quantize_microscaled."""
     fmt = _fp4_format(format)
     rows, cols, dev = _gated_rows(GU)
-    res, qp, bp, sp = _fp4_outputs(rows, cols, fmt, dev, out)
+    res, qp, bp, sp = _fp4_outputs(GU, rows, cols, fmt, dev, out)
     _call("fp4_silu_mul_quantize_microscaled", dev, GU.data_ptr(), rows, cols, fmt[0], qp, bp, sp,
           _row_status(status, dev))
     return res

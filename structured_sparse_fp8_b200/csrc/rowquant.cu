@@ -697,15 +697,16 @@ __device__ __forceinline__ uint32_t widen4(uint32_t four) {  // 4 codes in bits 
   return mag | sg;
 }
 
-__global__ void __launch_bounds__(256) unpack_kernel(const uint8_t *q, int64_t bytes, uint8_t *out) {
+// 16 bytes of codes a thread.
+__global__ void __launch_bounds__(256) unpack_kernel(const uint8_t *q, int64_t n, uint8_t *out) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t n = bytes / 8, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
-    const uint2 c = reinterpret_cast<const uint2 *>(q)[i];
-    reinterpret_cast<uint4 *>(out)[i] =
-        make_uint4(widen4(c.x & 0xFFFFu), widen4(c.x >> 16), widen4(c.y & 0xFFFFu), widen4(c.y >> 16));
-  }
+  if (i >= n) return;
+  const uint4 c = ld_row(reinterpret_cast<const uint16_t *>(q) + 8 * i);
+  uint4 *o = reinterpret_cast<uint4 *>(out) + 2 * i;
+  o[0] = make_uint4(widen4(c.x & 0xFFFFu), widen4(c.x >> 16), widen4(c.y & 0xFFFFu), widen4(c.y >> 16));
+  o[1] = make_uint4(widen4(c.z & 0xFFFFu), widen4(c.z >> 16), widen4(c.w & 0xFFFFu), widen4(c.w >> 16));
 }
 
 }  // namespace
@@ -715,8 +716,8 @@ cudaError_t launch_rowquant_norm(RowOut out, const RowQuantArgs &a, cudaStream_t
 cudaError_t launch_rowquant_gate(RowOut out, const RowQuantArgs &a, cudaStream_t st) { return launch<kSrcGate>(out, a, st); }
 
 cudaError_t launch_fp4_unpack(const uint8_t *q, int64_t bytes, uint8_t *out, cudaStream_t st) {
-  const int64_t want = (bytes / 8 + 255) / 256;
-  return launch_dependent(unpack_kernel, dim3(static_cast<unsigned>(want < 148 * 32 ? want : 148 * 32)), 256u, 0, st, q, bytes, out);
+  const int64_t n = bytes / 16;  // whole: rows hold multiples of 16 bytes
+  return launch_dependent(unpack_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), 256u, 0, st, q, n, out);
 }
 
 }  // namespace sp24
