@@ -462,7 +462,9 @@ int fp4_unpack_e4m3(const uint8_t *q, int64_t rows, int64_t cols, uint8_t *out, 
  * x and w the values code * block scale, fp32 accumulation, x_scale(m) =
  * x_scales[m] when x_per_token, else x_scales[0], or 1 when x_scales is NULL;
  * w_scale(n) likewise.  Xq u8 [M, K / 2], Wq u8 [N, K / 2], block scales in
- * the tiles above, of [M, K] and [N, K].  Y bf16 [M, N] must not alias an
+ * the tiles above (E4M3 ones without a sign; what the tiles hold outside the
+ * matrix does not matter), of [M, K] and [N, K].  Products below 2^-126 may
+ * count as zero.  Y bf16 [M, N] must not alias an
  * input.  No workspace; the same inputs give the same bits.  Shape rules:
  * 1 <= M <= 2^31 - 256, 8 <= N <= 2^31 - 256, N % 8 == 0, K >= 64, K % 64 == 0.
  */
@@ -483,8 +485,10 @@ int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const
  *   row), q u8 [rows, cols] = E4M3(y / scales[m]): an operand of
  *   sp24_gemm_packed_scaled.  cols % 16 == 0.
  * fp4_...: y quantised as fp4_quantize_microscaled quantises (cols % 32 == 0).
- * No workspace.  SP24_STATUS_NONFINITE when a row holds NaN/Inf or its sum of
- * squares leaves fp32's range; the outputs of that row alone are unspecified.
+ * No workspace.  Squares are summed in fp32 (a magnitude below about 1e-22
+ * adds nothing).  SP24_STATUS_NONFINITE when a row holds NaN/Inf, or when its
+ * sum of squares or a product h * weight leaves fp32's range; the outputs of
+ * that row alone are unspecified.
  * SP24_ERR_SHAPE also for an eps that is negative or not finite.
  */
 int fp8_rmsnorm_quantize_pertoken(const void *X, const void *residual, const void *weight, float eps, int64_t rows,

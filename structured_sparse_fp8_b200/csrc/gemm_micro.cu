@@ -28,6 +28,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "kernels.h"
@@ -706,17 +707,14 @@ __global__ void __launch_bounds__(Wide<BLOCK>::kThreads, 1)
 
 // ------------------------------------------------------------------ host
 
-// Clusters of `slices` SM pairs of the wide kernel that the device runs at once
-// (148 SMs hold 74, 33 and 22).
+// Clusters of `slices` SM pairs of the wide kernel that a device runs at once
+// (148 SMs hold 74, 33 and 22); asked once, with the kernel's shared memory
+// allowed.
 template <int BLOCK>
 int wide_clusters(int slices) {
   static int cap[kMaxWideSlices + 1] = {};
   static std::once_flag once;
   std::call_once(once, [] {
-    if (cudaFuncSetAttribute(wide_kernel<BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<BLOCK>::kSmem) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return;
-    }
     for (unsigned i = 1; i <= kMaxWideSlices; ++i) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * i, 1, 1);
@@ -771,11 +769,8 @@ bool make_maps(CUtensorMap *codes, CUtensorMap *scales, const uint8_t *q, const 
 template <int BLOCK, int BN>
 cudaError_t launch_narrow(const MicroGemmArgs &a, MicroParams p, cudaStream_t st) {
   using C = Narrow<BLOCK, BN>;
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(narrow_kernel<BLOCK, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  });
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t err = allow_shared(narrow_kernel<BLOCK, BN>, C::kSmem, ready);
   if (err != cudaSuccess) return err;
   p.tiles_n = (a.N + 127) / 128;
   p.tiles_m = (a.M + BN - 1) / BN;
@@ -800,6 +795,9 @@ cudaError_t launch_wide(const MicroGemmArgs &a, MicroParams p, cudaStream_t st) 
   p.tiles_n = (a.N + 255) / 256;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t err = allow_shared(wide_kernel<BLOCK>, Wide<BLOCK>::kSmem, ready);
+  if (err != cudaSuccess) return err;
   const int pairs = wide_clusters<BLOCK>(1);
   if (pairs < 1) return cudaErrorInvalidConfiguration;
   // few tiles: slices of K over the idle pairs.  A stage takes about 0.4 us

@@ -6,7 +6,23 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace sp24 {
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device;
+// `ready` has a bit for each device where that is done.
+template <typename... Args>
+cudaError_t allow_shared(void (*kernel)(Args...), uint32_t bytes, std::atomic<uint64_t> &ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // ---- rowquant.cu
 enum RowOut : int { kOutE4M3 = 0, kOutNvfp4 = 1, kOutMxfp4 = 2 };

@@ -31,7 +31,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
+#include <atomic>
 
 #include "micro_common.cuh"
 #include "micro_kernels.h"
@@ -625,12 +625,8 @@ bool launch_stream(const RowQuantArgs &a, cudaStream_t st, cudaError_t &err) {
   depth = depth > 4 ? 4 : depth;
   depth = depth > rounds ? rounds : depth;
   const StreamShape sh{static_cast<int>(depth), static_cast<uint32_t>(stage)};
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(stream_row_kernel<SRC, OUT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024 - 512);
-  });
-  err = attr;
+  static std::atomic<uint64_t> ready{0};
+  err = allow_shared(stream_row_kernel<SRC, OUT, T>, 226 * 1024 - 512, ready);
   if (err != cudaSuccess) return true;
   const int64_t most = static_cast<int64_t>(148 * per), grid = a.rows < most ? a.rows : most;
   err = launch_dependent(stream_row_kernel<SRC, OUT, T>, dim3(static_cast<unsigned>(grid)), T,
@@ -700,11 +696,12 @@ __device__ __forceinline__ uint32_t widen4(uint32_t four) {  // 4 codes in bits 
   return mag | sg;
 }
 
-// 16 bytes of codes a thread.
+// 16 bytes of codes a thread.  It does not release its dependents early: its
+// codes may be the weights of a dense FP8 GEMM, whose loads of them do not wait
+// for the kernel before.
 __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t *q, int64_t n, uint8_t *out) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   grid_dependency_wait();
-  grid_launch_dependents();
   if (i >= n) return;
   const uint4 c = ld_row(reinterpret_cast<const uint16_t *>(q) + 8 * i);
   uint4 *o = reinterpret_cast<uint4 *>(out) + 2 * i;

@@ -312,6 +312,40 @@ def test_gate(fmt, shape):
     assert int(st.item()) == 0
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("power", [-118, -100, -70, 60, 100, 118])
+@pytest.mark.parametrize("rows,cols", [(3, 96), (3, 4096), (1300, 8192), (2, 40032)])
+def test_rows_of_any_size(fmt, power, rows, cols):
+    """Values scaled by a power of two, through the norm's weight and the
+    gate's up projection: quotients of a row's values stay in range."""
+    few = slice(0, 3)                                       # rows that are checked
+    x = np.tile(WL.random_bits((3, cols), 71), (rows // 3 + 1, 1))[:rows]
+    up = WL.to_bf16_bits(O.bf16_to_f32(WL.random_bits((1, cols), 72)).astype(np.float64) * 2.0 ** power)
+    st = status()
+    y, _ = MO.rmsnorm(x[few], None, up[0], 1e-5)
+    gu = np.concatenate([x, np.tile(up, (rows, 1))], axis=1)
+    gy = MO.silu_mul(gu[few])
+    d = (1.173 * np.abs(O.bf16_to_f32(x[few]).astype(np.float64)) + 8) * 2 * U
+    X, W, GU = dev_bf16(x), dev_bf16(up[0]), dev_bf16(gu)
+    if fmt == "e4m3":
+        q, s, _ = sp().fp8_rmsnorm_quantize_pertoken(X, W, 1e-5, status=st)
+        check_e4m3(q[few], s[few], y, norm_error(cols))
+        q, s = sp().fp8_silu_mul_quantize_pertoken(GU, status=st)
+        check_e4m3(q[few], s[few], gy, d)
+    else:
+        n = min(rows, 3)
+
+        def first(b):                                       # the first rows' scales, as a matrix of their own
+            byts = rows_of(b, rows, cols, fmt)[:n]
+            return torch.from_numpy(MO.to_tiles(byts)).to(DEV)
+
+        q, b, s, _ = sp().fp4_rmsnorm_quantize_microscaled(X, W, 1e-5, fmt, status=st)
+        check_fp4(q[few], first(b), None if s is None else s[few], y, norm_error(cols), fmt)
+        q, b, s = sp().fp4_silu_mul_quantize_microscaled(GU, fmt, status=st)
+        check_fp4(q[few], first(b), None if s is None else s[few], gy, d, fmt)
+    assert int(st.item()) == 0
+
+
 def test_gate_flags_a_nonfinite_row():
     gu = WL.random_bits((4, 128), 12)
     good_q, good_s = sp().fp8_silu_mul_quantize_pertoken(dev_bf16(gu))
@@ -346,7 +380,10 @@ def dev_values(codes, byts, fmt):
 def check_product(y, xv, wv, xs, ws):
     """|y - ref| <= half a bf16 step of ref + what fp32 sums may lose: every
     product is exact (12 significant bits); the sum of K of them in groups of
-    64 is K / 64 + 64 roundings deep, a rounding taken as a whole fp32 step."""
+    64 is K / 64 + 64 roundings deep, a rounding taken as a whole fp32 step.
+    fp32's normal numbers end at 2^-126 and bf16's steps at 2^-133: K products
+    below the former (scale bytes of 0 stand for 2^-127) add up to K * 2^-126 at
+    most and may be dropped, and a result is off by half the latter."""
     k = xv.shape[1]
     scale = torch.ones(1, 1, dtype=torch.float64, device=DEV)
     if xs is not None:
@@ -355,8 +392,8 @@ def check_product(y, xv, wv, xs, ws):
         scale = scale * ws.double().reshape(1, -1)
     ref = xv @ wv.t() * scale
     mag = xv.abs() @ wv.abs().t() * scale.abs()
-    lost = (k / 64 + 64) * 2 * U * mag + 2 * U * ref.abs()
-    tol = 2.0 ** -8 * (ref.abs() + lost) + lost
+    lost = (k / 64 + 64) * 2 * U * mag + 2 * U * ref.abs() + k * 2.0 ** -126 * scale.abs()
+    tol = 2.0 ** -8 * (ref.abs() + lost) + lost + 2.0 ** -134
     off = (y.double() - ref).abs()
     ok = off <= tol
     assert bool(ok.all()), f"{int((~ok).sum())} of {ok.numel()} outside; first {torch.argwhere(~ok)[:4].tolist()}"
@@ -365,7 +402,7 @@ def check_product(y, xv, wv, xs, ws):
 PSHAPES = [(1, 8, 64), (1, 128, 256), (2, 136, 192), (3, 4104, 320), (8, 256, 4096), (16, 1000, 1024), (17, 512, 2112),
            (33, 384, 1024), (64, 2048, 512), (100, 264, 4160), (128, 4096, 448), (129, 520, 832), (256, 1024, 1088),
            (300, 2304, 2048), (515, 1160, 576), (1000, 520, 4160), (2050, 1032, 704), (1, 11008, 4096), (1, 96, 28672),
-           (70, 9000, 576), (200, 4360, 5120), (250, 6152, 5184), (600, 4104, 4160), (2000, 4096, 1024), (3000, 6152, 320)]
+           (70, 9000, 576), (200, 4360, 5120), (250, 6152, 5184), (600, 4104, 4160), (2000, 4096, 1024), (3000, 6152, 320), (17000, 8, 128), (9000, 40, 64)]
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
@@ -452,6 +489,33 @@ def test_long_rows_pass_32_bit_offsets():
     y = sp().fp4_gemm_microscaled(q, b, s, wq, wb, ws)
     y0 = sp().fp4_gemm_microscaled(q0, b0, s0, wq, wb, ws)
     torch.testing.assert_close(y[lo:].float(), y0.float(), rtol=2.0 ** -7, atol=1e-3)
+
+
+def test_result_past_32_bit_offsets():
+    """A result of more than 2^31 elements: its last rows as from a call of their own."""
+    m, n, k = 70016, 32768, 64
+    x = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+    w = torch.randn(n, k, device=DEV).to(torch.bfloat16)
+    wq = sp().fp4_quantize_microscaled(w, "mxfp4")
+    y = sp().fp4_gemm_microscaled(*sp().fp4_quantize_microscaled(x, "mxfp4"), *wq, "mxfp4")
+    tail = sp().fp4_gemm_microscaled(*sp().fp4_quantize_microscaled(x[-64:].contiguous(), "mxfp4"), *wq, "mxfp4")
+    assert torch.equal(y[-64:], tail)        # one MMA step deep: no order of sums
+
+
+def test_unpacked_codes_feed_the_dense_fp8_product():
+    """FP4 weights widened to E4M3, in front of the dense FP8 GEMM right away."""
+    x, w = dev_bf16(WL.random_bits((64, 512), 81)), dev_bf16(WL.random_bits((256, 512), 82, scale=0.02))
+    xq, sx = sp().fp8_quantize_pertensor(x)
+    wq, sw = sp().fp4_quantize_pertensor(w)
+    wide = sp().fp4_unpack_e4m3(wq)
+    want = sp().fp8_gemm_dense(xq, sx, wide, sw)
+    torch.cuda.synchronize()
+    ref, bound = O.gemm_ref(O.e4m3_decode(xq.cpu().numpy()), O.e2m1_decode(unpack(wq)), sx.item(), sw.item())
+    assert O.within_tolerance(O.bf16_to_f32(bits_of(want)).astype(np.float64), ref, bound).all()
+    for _ in range(20):
+        buf = torch.zeros_like(wide)
+        y = sp().fp8_gemm_dense(xq, sx, sp().fp4_unpack_e4m3(wq, out=buf), sw)
+        assert torch.equal(y, want)
 
 
 # ------------------------------------------------------------------ use together
