@@ -159,12 +159,15 @@ struct Narrow {
   static constexpr uint32_t kStageBytes = kSfbOff + kSfBytes;
   static constexpr bool kOwnRoom = BN <= 32;
   static constexpr uint32_t kPartBytes = most_tokens(BN) * 512;
-  // CTAs that share an SM.  The smallest tiles leave room for the next call's
-  // CTAs, whose start (barriers, tensor memory, descriptors: about 1 us) then
-  // hides behind this call.
-  static constexpr int kPerSm = BN <= 16 ? 4 : BN <= 32 ? 3 : 2;
-  static constexpr uint32_t kBudget = kPerSm == 4 ? 57344 : kPerSm == 3 ? 75776 : 114688;
-  static constexpr int kStages = (kBudget - 3072 - (kOwnRoom ? kPartBytes : 0)) / kStageBytes;
+  // Two CTAs on an SM, so that one starts (barriers, tensor memory,
+  // descriptors: about 1 us) while the other works.  (Four of two stages each,
+  // for BN = 16, held fewer bytes in flight: 1 x 11008 x 4096 7.5 us against
+  // 7.2, 1 x 4096 x 14336 9.2 against 8.5.)
+  static constexpr int kPerSm = 2;
+  static constexpr int kStages = (112 * 1024 - 3072 - (kOwnRoom ? kPartBytes : 0)) / kStageBytes;
+  // CTAs that a call is cut into, and stages of a slice at least
+  static constexpr int kCtas = BN <= 16 ? 192 : 2 * kNarrowTiles;
+  static constexpr int kSliceStages = BN <= 32 ? 3 : 4;
   static constexpr uint32_t kPartOff = kOwnRoom ? kStages * kStageBytes : BN * 512;
   static constexpr uint32_t kBarOff = kStages * kStageBytes + (kOwnRoom ? kPartBytes : 0);
   static constexpr uint32_t kScaleOff = kBarOff + 512;  // the tile's token scales
@@ -774,12 +777,15 @@ cudaError_t launch_narrow(const MicroGemmArgs &a, MicroParams p, cudaStream_t st
   if (err != cudaSuccess) return err;
   p.tiles_n = (a.N + 127) / 128;
   p.tiles_m = (a.M + BN - 1) / BN;
-  // K slices: as many as leave every CTA resident at once, two on an SM
-  // (clusters of 3 to 8 CTAs fill 132 of the 148)
+  // K slices, cold weights: 1 x 11008 x 4096 (86 tiles) 7.2 us with 2, 7.6 with
+  // 3, 10.4 with 4 (a second wave); 1 x 4096 x 14336 (32 tiles) 8.5 with 6, 9.7
+  // with 3; 64 x 11008 x 4096 9.7 with 3, 10.0 with 2; 64 x 4096 x 4096 6.7 with
+  // 4 (4 stages each), 7.9 with 8.
   const int64_t tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_m;
-  int64_t s = 2 * kNarrowTiles / tiles;
-  s = s < 1 ? 1 : s > kMaxSlices ? kMaxSlices : s;
-  if (s > p.stages) s = p.stages;
+  int64_t s = C::kCtas / tiles;
+  if (s > p.stages / C::kSliceStages) s = p.stages / C::kSliceStages;
+  if (s > kMaxSlices) s = kMaxSlices;
+  if (s < 1) s = 1;
   p.slices = static_cast<int>(s);
   CUtensorMap tm[4];
   if (!make_maps(&tm[0], &tm[2], a.wq, a.wb, a.N, a.K, BLOCK, 128) ||
