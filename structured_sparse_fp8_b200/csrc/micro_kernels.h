@@ -38,6 +38,7 @@ struct RowQuantArgs {
   float *scales;             // E4M3 and nvfp4: one per row
   int64_t rows, cols;
   int32_t *status;
+  bool wide;                 // x, residual and residual_out are 32-byte aligned (set by the launch)
 };
 
 cudaError_t launch_rowquant_plain(RowOut out, const RowQuantArgs &a, cudaStream_t st);

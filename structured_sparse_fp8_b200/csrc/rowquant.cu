@@ -45,20 +45,47 @@ namespace {
 
 enum RowSrc : int { kSrcPlain = 0, kSrcNorm = 1, kSrcGate = 2 };
 
-constexpr int kChunk = 8;                    // elements per thread and load
+constexpr int kChunk = 16;                   // elements a thread takes at a time
 constexpr int kWarpRows = 8;                 // rows of a CTA in the warp-per-row form
 constexpr float kRowFloor = 0x1.5p-89f;      // 2688 * 2^-100
 constexpr int64_t kFewRows = 2 * 148;         // two CTAs an SM
-constexpr int64_t kStreamRows = 8 * 148, kStreamChunks = 768;  // what the streamed form starts from
+constexpr int64_t kStreamRows = 8 * 148, kStreamChunks = 384;  // what the streamed form starts from
 constexpr float kInf = __builtin_huge_valf();
 
-// ld.global (not .nc: residual_out may be x or residual), kept out of L1
-__device__ __forceinline__ uint4 ld_row(const uint16_t *p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 16 bf16 values.
+struct Raw {
+  uint32_t w[8];
+};
+// ld.global and not .nc: residual_out may be x or residual.  One 32-byte load
+// where the row's address allows (all lanes alike), else two of 16 bytes,
+// through L1, where they meet.
+__device__ __forceinline__ Raw ld_row(const uint16_t *p, bool wide) {
+  Raw r;
+  if (wide) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+                 : "l"(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r.w[4 * i]), "=r"(r.w[4 * i + 1]), "=r"(r.w[4 * i + 2]), "=r"(r.w[4 * i + 3])
+                   : "l"(p + 8 * i));
+  }
+  return r;
+}
+__device__ __forceinline__ void st_row(uint16_t *p, const Raw &r, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]),
+                 "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7]), "l"(p)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+  }
+}
+__device__ __forceinline__ Raw raw_of(const uint4 &a, const uint4 &b) {
+  return Raw{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 
 // Two fp32 values in a register pair, and the packed operations on them: such
@@ -91,21 +118,20 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 }
 __device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
 
-// 8 values of a chunk.
+// 16 values of a chunk.
 struct Chunk {
-  f2 v[4];
+  f2 v[8];
   __device__ __forceinline__ void scale(float m) {
     const f2 mm = both(m);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], mm);
+    for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], mm);
   }
 };
 
-__device__ __forceinline__ Chunk unpack8(const uint4 &a) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ Chunk unpack(const Raw &r) {
   Chunk c;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c.v[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  for (int i = 0; i < 8; ++i) c.v[i] = pack2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
   return c;
 }
 
@@ -137,35 +163,35 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-// The largest of `so_far` (>= 0) and the chunk's magnitudes.
-__device__ __forceinline__ float max_abs8(const Chunk &c, float so_far = 0.0f) {
+// The largest magnitude of the chunk.
+__device__ __forceinline__ float max_abs(const Chunk &c) {
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const float2 v = split2(c.v[i]);
-    so_far = max_abs3(so_far, v.x, v.y);
+    m = max_abs3(m, v.x, v.y);
   }
-  return so_far;
+  return m;
 }
 
-// bf16(x + r) of 8 values: the sum of two bf16 values rounded once (fp32 holds
-// every such sum that is near a rounding boundary exactly)
-__device__ __forceinline__ uint4 add_bf16(const uint4 &x, const uint4 &r) {
-  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {r.x, r.y, r.z, r.w};
-  uint32_t o[4];
+// bf16(x + r): the sum of two bf16 values rounded once (fp32 holds every such
+// sum that is near a rounding boundary exactly)
+__device__ __forceinline__ Raw add_bf16(const Raw &x, const Raw &r) {
+  Raw o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&a[i]), *reinterpret_cast<const __nv_bfloat162 *>(&b[i]));
-    o[i] = *reinterpret_cast<const uint32_t *>(&h);
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&x.w[i]), *reinterpret_cast<const __nv_bfloat162 *>(&r.w[i]));
+    o.w[i] = *reinterpret_cast<const uint32_t *>(&h);
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  return o;
 }
 
 // z = h * w, and the sum of h^2
-__device__ __forceinline__ Chunk norm_values(const uint4 &h, const uint4 &w, f2 &sum) {
-  Chunk y = unpack8(h);
-  const Chunk ww = unpack8(w);
+__device__ __forceinline__ Chunk norm_values(const Raw &h, const Raw &w, f2 &sum) {
+  Chunk y = unpack(h);
+  const Chunk ww = unpack(w);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     sum = fma2(y.v[i], y.v[i], sum);
     y.v[i] = mul2(y.v[i], ww.v[i]);
   }
@@ -173,11 +199,11 @@ __device__ __forceinline__ Chunk norm_values(const uint4 &h, const uint4 &w, f2 
 }
 
 // g / (1 + exp(-g)) * u.  Where exp(-g) leaves fp32's range its reciprocal is 0.
-__device__ __forceinline__ Chunk gate_values(const uint4 &gv, const uint4 &uv) {
-  Chunk g = unpack8(gv);
-  const Chunk u = unpack8(uv);
+__device__ __forceinline__ Chunk gate_values(const Raw &gv, const Raw &uv) {
+  Chunk g = unpack(gv);
+  const Chunk u = unpack(uv);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const float2 a = split2(mul2(g.v[i], both(-1.4426950408889634f)));
     float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(a.x));
@@ -211,20 +237,21 @@ template <int SRC>
 __device__ __forceinline__ Chunk chunk_values(const RowQuantArgs &p, const Row &row, int c, bool first, f2 &sum) {
   const int at = c * kChunk;
   if constexpr (SRC == kSrcPlain) {
-    return unpack8(ld_row(row.x + at));
+    return unpack(ld_row(row.x + at, p.wide));
   } else if constexpr (SRC == kSrcNorm) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.weight) + c);
-    uint4 h;
+    const uint4 *w = reinterpret_cast<const uint4 *>(p.weight) + 2 * c;
+    const uint4 w0 = __ldg(w), w1 = __ldg(w + 1);
+    Raw h;
     if (first && p.residual) {
-      const uint4 x = ld_row(row.x + at), r = ld_row(row.residual + at);
+      const Raw x = ld_row(row.x + at, p.wide), r = ld_row(row.residual + at, p.wide);
       h = add_bf16(x, r);
-      *reinterpret_cast<uint4 *>(row.h + at) = h;
+      st_row(row.h + at, h, p.wide);
     } else {
-      h = ld_row((p.residual ? row.h : row.x) + at);
+      h = ld_row((p.residual ? row.h : row.x) + at, p.wide);
     }
-    return norm_values(h, w, sum);
+    return norm_values(h, raw_of(w0, w1), sum);
   } else {
-    const uint4 g = ld_row(row.x + at), u = ld_row(row.residual + at);
+    const Raw g = ld_row(row.x + at, p.wide), u = ld_row(row.residual + at, p.wide);
     return gate_values(g, u);
   }
 }
@@ -304,7 +331,7 @@ __device__ __forceinline__ void encode_chunk(const RowQuantArgs &p, const Row &r
   float v[kChunk];
   auto spread = [&] {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const float2 s = split2(y.v[i]);
       v[2 * i] = s.x, v[2 * i + 1] = s.y;
     }
@@ -312,12 +339,13 @@ __device__ __forceinline__ void encode_chunk(const RowQuantArgs &p, const Row &r
   if constexpr (OUT == kOutE4M3) {
     y.scale(r.mul);
     spread();
-    if (on) *reinterpret_cast<uint2 *>(row.q + c * kChunk) = make_uint2(e4m3_codes4(v), e4m3_codes4(v + 4));
+    if (on)
+      *reinterpret_cast<uint4 *>(row.q + c * kChunk) =
+          make_uint4(e4m3_codes4(v), e4m3_codes4(v + 4), e4m3_codes4(v + 8), e4m3_codes4(v + 12));
   } else {
     float mul;
     uint32_t code;
     if constexpr (OUT == kOutNvfp4) {
-      top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       code = e4m3_code_positive(settle_scale<SRC>(top * r.sf));
       mul = code == 0u ? 0.0f : r.mul * rcp_approx(e4m3_value(code));
     } else {
@@ -326,7 +354,6 @@ __device__ __forceinline__ void encode_chunk(const RowQuantArgs &p, const Row &r
         y.scale(r.mul);
       }
       top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       if (!(top < kInf) && p.status) atomicOr(p.status, SP24_STATUS_NONFINITE);
       code = static_cast<uint32_t>(max(static_cast<int>(__float_as_uint(top) >> 23) - 2, 0));
       mul = __uint_as_float((254u - code) << 23);
@@ -334,14 +361,14 @@ __device__ __forceinline__ void encode_chunk(const RowQuantArgs &p, const Row &r
     if constexpr (OUT == kOutNvfp4 && SRC == kSrcPlain) {
       const f2 m = both(mul), up = both(kSettle), down = both(-kSettle);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y.v[i] = add2(fma2(y.v[i], m, up), down);
+      for (int i = 0; i < 8; ++i) y.v[i] = add2(fma2(y.v[i], m, up), down);
     } else {
       y.scale(mul);
     }
     spread();
-    if (on) *reinterpret_cast<uint32_t *>(row.q + c * 4) = e2m1_codes8(v);
+    if (on) *reinterpret_cast<uint2 *>(row.q + c * 8) = make_uint2(e2m1_codes8(v), e2m1_codes8(v + 8));
     // four block scales to a word (absent blocks of a last tile are zero)
-    constexpr int lanes = OUT == kOutNvfp4 ? 2 : 4;  // per block
+    constexpr int lanes = OUT == kOutNvfp4 ? 1 : 2;  // per block
     uint32_t word = on ? code << (8 * (lane / lanes & 3)) : 0u;
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, lanes);
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * lanes);
@@ -383,7 +410,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
   float top[kLive], sum = 0.0f, amax = 0.0f;
   auto take = [&](int c, Chunk &v, float &most) {
     v = chunk_values<SRC>(p, at, c, true, sums);
-    most = max_abs8(v);
+    most = max_abs(v);
     if constexpr (kNeedMax) amax = max_nan(amax, most);
   };
   if constexpr (NC > 0) {
@@ -438,7 +465,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
       Chunk v{};
       f2 none = 0;
       if (c < chunks) v = chunk_values<SRC>(p, at, c, false, none);
-      put(c, c < chunks, v, max_abs8(v));
+      put(c, c < chunks, v, max_abs(v));
     }
   }
 }
@@ -492,7 +519,7 @@ __global__ void __launch_bounds__(T, 1024 / T) stream_row_kernel(const RowQuantA
     for (int s = 0; s < shape.depth; ++s)
       if (first + s * step < p.rows) load(first + s * step, s);
   if constexpr (SRC == kSrcNorm) {
-    for (int c = t; c < chunks; c += T) const_cast<uint4 *>(weight)[c] = __ldg(reinterpret_cast<const uint4 *>(p.weight) + c);
+    for (int c = t; c < 2 * chunks; c += T) const_cast<uint4 *>(weight)[c] = __ldg(reinterpret_cast<const uint4 *>(p.weight) + c);
     __syncthreads();
   }
   int s = 0;
@@ -503,36 +530,39 @@ __global__ void __launch_bounds__(T, 1024 / T) stream_row_kernel(const RowQuantA
     uint4 *in2 = reinterpret_cast<uint4 *>(ring + s * shape.stage + half);
     mbar_wait(&full[s], phase, p.status);
     // the values of chunk c: first read, and read again
+    auto raw = [](const uint4 *from, int c) { return raw_of(from[2 * c], from[2 * c + 1]); };
     auto first_values = [&](int c, f2 &sums) {
       if constexpr (SRC == kSrcPlain) {
-        return unpack8(in[c]);
+        return unpack(raw(in, c));
       } else if constexpr (SRC == kSrcGate) {
-        return gate_values(in[c], in2[c]);
+        return gate_values(raw(in, c), raw(in2, c));
       } else {
-        uint4 h = in[c];
+        Raw h = raw(in, c);
         if (two) {
-          h = add_bf16(h, in2[c]);
-          *reinterpret_cast<uint4 *>(at.h + c * kChunk) = h;
+          h = add_bf16(h, raw(in2, c));
+          st_row(at.h + c * kChunk, h, p.wide);
         }
-        return norm_values(h, weight[c], sums);
+        return norm_values(h, raw(weight, c), sums);
       }
     };
     auto keep = [&](int c, const Chunk &y) {
       if (two) {
-        in[c] = *reinterpret_cast<const uint4 *>(&y.v[0]);
-        in2[c] = *reinterpret_cast<const uint4 *>(&y.v[2]);
+        const uint4 *v = reinterpret_cast<const uint4 *>(y.v);
+        in[2 * c] = v[0], in[2 * c + 1] = v[1];
+        in2[2 * c] = v[2], in2[2 * c + 1] = v[3];
       }
     };
     auto kept = [&](int c) {
       Chunk y;
       if (SRC != kSrcPlain && two) {
-        *reinterpret_cast<uint4 *>(&y.v[0]) = in[c];
-        *reinterpret_cast<uint4 *>(&y.v[2]) = in2[c];
+        uint4 *v = reinterpret_cast<uint4 *>(y.v);
+        v[0] = in[2 * c], v[1] = in[2 * c + 1];
+        v[2] = in2[2 * c], v[3] = in2[2 * c + 1];
       } else if constexpr (SRC == kSrcNorm) {
         f2 none = 0;
-        y = norm_values(in[c], weight[c], none);
+        y = norm_values(raw(in, c), raw(weight, c), none);
       } else {
-        y = unpack8(in[c]);
+        y = unpack(raw(in, c));
       }
       return y;
     };
@@ -543,7 +573,7 @@ __global__ void __launch_bounds__(T, 1024 / T) stream_row_kernel(const RowQuantA
 #pragma unroll 2
       for (int c = t; c < chunks; c += T) {
         const Chunk y = first_values(c, sums);
-        if constexpr (kNeedMax) amax = max_abs8(y, amax);
+        if constexpr (kNeedMax) amax = max_nan(amax, max_abs(y));
         if constexpr (SRC != kSrcPlain) keep(c, y);
       }
       if constexpr (kNeedMax) amax = warp_max(amax);
@@ -572,7 +602,7 @@ __global__ void __launch_bounds__(T, 1024 / T) stream_row_kernel(const RowQuantA
           y = first_values(c, none);
       }
       if (r.pre != 1.0f) y.scale(r.pre);
-      encode_chunk<SRC, OUT>(p, at, c, c < chunks, r, y, max_abs8(y));
+      encode_chunk<SRC, OUT>(p, at, c, c < chunks, r, y, max_abs(y));
     }
     // the row's place in the ring is free: its next row
     if constexpr (SRC != kSrcPlain && (kNeedMax || kNeedSum)) fence_proxy_async_smem();
@@ -647,38 +677,36 @@ template <int SRC, int OUT>
 cudaError_t launch_out(const RowQuantArgs &a, cudaStream_t st) {
   const int64_t rows = OUT == kOutE4M3 ? a.rows : (a.rows + 127) / 128 * 128;
   const int64_t chunks = a.cols / kChunk;
-  if (chunks <= 128) {
+  if (chunks <= 64) {
     const unsigned grid = static_cast<unsigned>((rows + kWarpRows - 1) / kWarpRows);
     if (chunks <= 32) return launch_form<SRC, OUT, 1, true>(a, grid, 32 * kWarpRows, st);
-    return launch_form<SRC, OUT, 4, true>(a, grid, 32 * kWarpRows, st);
+    return launch_form<SRC, OUT, 2, true>(a, grid, 32 * kWarpRows, st);
   }
   const unsigned grid = static_cast<unsigned>(rows);
   if constexpr (OUT == kOutMxfp4 && SRC != kSrcNorm) {
-    // nothing to reduce over the row: CTAs of up to 256 threads, one or two
-    // chunks each (plain, 12288 x 4096: 31.1, 27.4 us, four 38.3; gate, 64 x
-    // 11008: 2.2, 2.8 us)
-    const int nc = a.rows <= kFewRows ? 1 : 2;
-    const int64_t segs = (chunks + 256 * nc - 1) / (256 * nc);
-    const unsigned threads = static_cast<unsigned>((chunks + 32 * nc * segs - 1) / (32 * nc * segs) * 32);
-    return nc == 1 ? launch_form<SRC, OUT, 1, false>(a, grid, threads, st, static_cast<unsigned>(segs))
-                   : launch_form<SRC, OUT, 2, false>(a, grid, threads, st, static_cast<unsigned>(segs));
+    // nothing to reduce over the row: CTAs of up to 256 threads, a chunk each
+    const int64_t segs = (chunks + 255) / 256;
+    const unsigned threads = static_cast<unsigned>((chunks + 32 * segs - 1) / (32 * segs) * 32);
+    return launch_form<SRC, OUT, 1, false>(a, grid, threads, st, static_cast<unsigned>(segs));
   } else {
     if (a.rows >= kStreamRows && chunks >= kStreamChunks) {
       cudaError_t err;
-      if (chunks <= 1152 ? launch_stream<SRC, OUT, 256>(a, st, err) : launch_stream<SRC, OUT, 512>(a, st, err)) return err;
+      if (chunks <= 576 ? launch_stream<SRC, OUT, 256>(a, st, err) : launch_stream<SRC, OUT, 512>(a, st, err)) return err;
     }
-    if (chunks > 4 * 1024) return launch_form<SRC, OUT, 0, false>(a, grid, 1024, st);
-    // few rows: as many threads on each as there are chunks
-    const int nc = chunks <= 1024 && a.rows <= kFewRows ? 1 : chunks <= (a.rows <= kFewRows ? 2048 : 1024) ? 2 : 4;
+    if (chunks > 2 * 1024) return launch_form<SRC, OUT, 0, false>(a, grid, 1024, st);
+    const int nc = chunks <= 512 || (chunks <= 1024 && a.rows <= kFewRows) ? 1 : 2;
     const unsigned threads = static_cast<unsigned>((chunks + 32 * nc - 1) / (32 * nc) * 32);
     if (nc == 1) return launch_form<SRC, OUT, 1, false>(a, grid, threads, st);
-    if (nc == 2) return launch_form<SRC, OUT, 2, false>(a, grid, threads, st);
-    return launch_form<SRC, OUT, 4, false>(a, grid, threads, st);
+    return launch_form<SRC, OUT, 2, false>(a, grid, threads, st);
   }
 }
 
 template <int SRC>
-cudaError_t launch(RowOut out, const RowQuantArgs &a, cudaStream_t st) {
+cudaError_t launch(RowOut out, RowQuantArgs a, cudaStream_t st) {
+  // rows are multiples of 32 bytes, so their addresses are aligned as the bases
+  const uintptr_t bases = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
+                          reinterpret_cast<uintptr_t>(a.residual_out);
+  a.wide = bases % 32 == 0;
   if (out == kOutNvfp4) return launch_out<SRC, kOutNvfp4>(a, st);
   if (out == kOutMxfp4) return launch_out<SRC, kOutMxfp4>(a, st);
   if constexpr (SRC == kSrcPlain)
@@ -703,7 +731,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t *q, int64_t n
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   grid_dependency_wait();
   if (i >= n) return;
-  const uint4 c = ld_row(reinterpret_cast<const uint16_t *>(q) + 8 * i);
+  const uint4 c = __ldcs(reinterpret_cast<const uint4 *>(q) + i);
   uint4 *o = reinterpret_cast<uint4 *>(out) + 2 * i;
   o[0] = make_uint4(widen4(c.x & 0xFFFFu), widen4(c.x >> 16), widen4(c.y & 0xFFFFu), widen4(c.y >> 16));
   o[1] = make_uint4(widen4(c.z & 0xFFFFu), widen4(c.z >> 16), widen4(c.w & 0xFFFFu), widen4(c.w >> 16));

@@ -346,6 +346,34 @@ def test_rows_of_any_size(fmt, power, rows, cols):
     assert int(st.item()) == 0
 
 
+@pytest.mark.parametrize("rows,cols", [(3, 96), (5, 4096), (1300, 8192), (2, 40032)])
+def test_inputs_aligned_to_16_bytes_only(rows, cols):
+    """Tensors that start 16 bytes into a 32-byte line give what others give."""
+    def shifted(t):
+        buf = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)
+        v = buf[8:].view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 32 == 16
+        return v
+
+    x, r = dev_bf16(WL.random_bits((rows, cols), 91)), dev_bf16(WL.random_bits((rows, cols), 92))
+    gu, w = dev_bf16(WL.random_bits((rows, 2 * cols), 93)), dev_bf16(WL.random_bits((1, cols), 94)[0])
+    m = sp()
+    for fmt in ("nvfp4", "mxfp4"):
+        for a, b in zip(m.fp4_quantize_microscaled(x, fmt), m.fp4_quantize_microscaled(shifted(x), fmt)):
+            assert a is None or torch.equal(a, b)
+        for a, b in zip(m.fp4_silu_mul_quantize_microscaled(gu, fmt), m.fp4_silu_mul_quantize_microscaled(shifted(gu), fmt)):
+            assert a is None or torch.equal(a, b)
+        for a, b in zip(m.fp4_rmsnorm_quantize_microscaled(x, w, 1e-5, fmt, residual=r),
+                        m.fp4_rmsnorm_quantize_microscaled(x, shifted(w), 1e-5, fmt, residual=shifted(r))):
+            assert a is None or torch.equal(a, b)
+    for a, b in zip(m.fp8_rmsnorm_quantize_pertoken(x, w, 1e-5, residual=r),
+                    m.fp8_rmsnorm_quantize_pertoken(x, w, 1e-5, residual=r, residual_out=shifted(x))):
+        assert torch.equal(a, b)
+    for a, b in zip(m.fp8_silu_mul_quantize_pertoken(gu), m.fp8_silu_mul_quantize_pertoken(shifted(gu))):
+        assert torch.equal(a, b)
+
+
 def test_gate_flags_a_nonfinite_row():
     gu = WL.random_bits((4, 128), 12)
     good_q, good_s = sp().fp8_silu_mul_quantize_pertoken(dev_bf16(gu))
