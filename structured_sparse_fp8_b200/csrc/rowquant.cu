@@ -20,18 +20,22 @@
 // (exact in fp32), sum h^2 and amax|z| come from one pass over the row, and
 // rstd enters the row's scale only.
 //
-// Such stages read and write each element once and are bound by memory.  A
-// row is held in registers from its one read to its last write, 8 elements
-// (16 bytes) per thread and load, neighbouring threads on neighbouring
-// chunks: a warp per row up to 1024 columns, a CTA of as many warps as the row
-// needs up to 32768, and beyond that a CTA that reads the row again for the
-// second pass.  Lanes share a block's largest value and pack four block
-// scales to a word by shuffles.
+// Such stages read and write each element once and are bound by memory, and
+// next by instruction issue: a thread takes 16 elements at a time (a block of
+// nvfp4, half one of mxfp4, a 32-byte access), so that a block's scale is
+// worked out once, and calculates on packed pairs.  A row is held in registers
+// from its one read to its last write: a warp per row up to 1024 columns, a
+// CTA of as many warps as the row needs up to 32768, and beyond that a CTA
+// that reads the row again for the second pass.  (8 elements a thread: norm to
+// E4M3, 4096 x 4096, 21.4 us against 18.9; quantiser to nvfp4, 12288 x 4096,
+// 37 against 29.  Rows brought ahead into shared memory by bulk copies of CTAs
+// that stay: 43 us against 35 for the norm at 4096 x 8192, 66 against 65 at
+// 4096 x 14336.)  Measured with cold inputs: norm to E4M3, 4096 x 4096, 18.9 us
+// (6.2 TB/s), 1 x 4096 1.9 us; gate to mxfp4, 4096 x 14336, 42.7 us (6.2 TB/s);
+// quantiser to mxfp4, 12288 x 4096, 23.2 us (5.5 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-
-#include <atomic>
 
 #include "micro_common.cuh"
 #include "micro_kernels.h"
@@ -48,8 +52,6 @@ enum RowSrc : int { kSrcPlain = 0, kSrcNorm = 1, kSrcGate = 2 };
 constexpr int kChunk = 16;                   // elements a thread takes at a time
 constexpr int kWarpRows = 8;                 // rows of a CTA in the warp-per-row form
 constexpr float kRowFloor = 0x1.5p-89f;      // 2688 * 2^-100
-constexpr int64_t kFewRows = 2 * 148;         // two CTAs an SM
-constexpr int64_t kStreamRows = 8 * 148, kStreamChunks = 384;  // what the streamed form starts from
 constexpr float kInf = __builtin_huge_valf();
 
 // 16 bf16 values.
@@ -470,153 +472,6 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
   }
 }
 
-// Many rows: CTAs stay and take rows blockIdx.x, blockIdx.x + gridDim.x, ...,
-// whose inputs bulk copies bring into a ring of `depth` rows in shared memory
-// ahead of time, so that loads never wait for a row's arithmetic, and a
-// thread's offsets are worked out once.  Between the passes a row's values
-// stay in its place in the ring: as fp32 where two bf16 inputs made room
-// (norm with a residual, gate), else as they came.
-struct StreamShape {
-  int depth;
-  uint32_t stage;   // bytes of a row's inputs
-};
-constexpr uint32_t kStreamBars = 128;  // barriers and their padding in front of the ring
-
-template <int SRC, int OUT, int T>
-__global__ void __launch_bounds__(T, 1024 / T) stream_row_kernel(const RowQuantArgs p, const StreamShape shape) {
-  constexpr bool kNeedMax = OUT != kOutMxfp4, kNeedSum = SRC == kSrcNorm;
-  constexpr int kWarps = T / 32;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 red[2][kWarps];
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem);
-  uint8_t *ring = smem + kStreamBars;
-  const uint4 *weight = reinterpret_cast<const uint4 *>(ring + shape.depth * shape.stage);
-  const int t = static_cast<int>(threadIdx.x), lane = t & 31;
-  const int chunks = static_cast<int>(p.cols / kChunk);
-  const int tiles = static_cast<int>(OUT == kOutNvfp4 ? (p.cols + 63) / 64 : (p.cols + 127) / 128);
-  const uint32_t half = static_cast<uint32_t>(p.cols) * 2;  // bytes of one bf16 row
-  const bool two = SRC == kSrcGate || (SRC == kSrcNorm && p.residual);
-  const uint64_t policy = l2_policy_evict_first();
-  auto load = [&](int64_t row, int s) {
-    mbar_arrive_expect_tx(&full[s], shape.stage);
-    uint8_t *dst = ring + s * shape.stage;
-    if constexpr (SRC == kSrcGate) {
-      bulk_load_g2s(dst, p.x + row * 2 * p.cols, 2 * half, &full[s], policy);
-    } else {
-      bulk_load_g2s(dst, p.x + row * p.cols, half, &full[s], policy);
-      if (SRC == kSrcNorm && p.residual) bulk_load_g2s(dst + half, p.residual + row * p.cols, half, &full[s], policy);
-    }
-  };
-  if (t == 0) {
-    for (int s = 0; s < shape.depth; ++s) mbar_init(&full[s], 1);
-    fence_mbar_init();
-  }
-  __syncthreads();
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int64_t first = blockIdx.x, step = gridDim.x;
-  if (t == 0)
-    for (int s = 0; s < shape.depth; ++s)
-      if (first + s * step < p.rows) load(first + s * step, s);
-  if constexpr (SRC == kSrcNorm) {
-    for (int c = t; c < 2 * chunks; c += T) const_cast<uint4 *>(weight)[c] = __ldg(reinterpret_cast<const uint4 *>(p.weight) + c);
-    __syncthreads();
-  }
-  int s = 0;
-  uint32_t phase = 0;
-  for (int64_t row = first, i = 0; row < p.rows; row += step, ++i) {
-    const Row at = row_of<SRC, OUT>(p, row, tiles);
-    uint4 *in = reinterpret_cast<uint4 *>(ring + s * shape.stage);
-    uint4 *in2 = reinterpret_cast<uint4 *>(ring + s * shape.stage + half);
-    mbar_wait(&full[s], phase, p.status);
-    // the values of chunk c: first read, and read again
-    auto raw = [](const uint4 *from, int c) { return raw_of(from[2 * c], from[2 * c + 1]); };
-    auto first_values = [&](int c, f2 &sums) {
-      if constexpr (SRC == kSrcPlain) {
-        return unpack(raw(in, c));
-      } else if constexpr (SRC == kSrcGate) {
-        return gate_values(raw(in, c), raw(in2, c));
-      } else {
-        Raw h = raw(in, c);
-        if (two) {
-          h = add_bf16(h, raw(in2, c));
-          st_row(at.h + c * kChunk, h, p.wide);
-        }
-        return norm_values(h, raw(weight, c), sums);
-      }
-    };
-    auto keep = [&](int c, const Chunk &y) {
-      if (two) {
-        const uint4 *v = reinterpret_cast<const uint4 *>(y.v);
-        in[2 * c] = v[0], in[2 * c + 1] = v[1];
-        in2[2 * c] = v[2], in2[2 * c + 1] = v[3];
-      }
-    };
-    auto kept = [&](int c) {
-      Chunk y;
-      if (SRC != kSrcPlain && two) {
-        uint4 *v = reinterpret_cast<uint4 *>(y.v);
-        v[0] = in[2 * c], v[1] = in[2 * c + 1];
-        v[2] = in2[2 * c], v[3] = in2[2 * c + 1];
-      } else if constexpr (SRC == kSrcNorm) {
-        f2 none = 0;
-        y = norm_values(raw(in, c), raw(weight, c), none);
-      } else {
-        y = unpack(raw(in, c));
-      }
-      return y;
-    };
-    float rstd = 1.0f, amax = 0.0f;
-    if constexpr (kNeedMax || kNeedSum) {
-      float sum = 0.0f;
-      f2 sums = 0;
-#pragma unroll 2
-      for (int c = t; c < chunks; c += T) {
-        const Chunk y = first_values(c, sums);
-        if constexpr (kNeedMax) amax = max_nan(amax, max_abs(y));
-        if constexpr (SRC != kSrcPlain) keep(c, y);
-      }
-      if constexpr (kNeedMax) amax = warp_max(amax);
-      if constexpr (kNeedSum) sum = warp_sum(split2(sums).x + split2(sums).y);
-      if (lane == 0) red[i & 1][t >> 5] = make_float2(amax, sum);
-      __syncthreads();
-      const float2 v = lane < kWarps ? red[i & 1][lane] : make_float2(0.0f, 0.0f);
-      if constexpr (kNeedMax) amax = warp_max(v.x);
-      if constexpr (kNeedSum) {
-        sum = warp_sum(v.y);
-        const float ms = __fdiv_rn(sum, static_cast<float>(p.cols)) + p.eps;
-        rstd = ms > 0.0f ? __frsqrt_rn(ms) : 0.0f;
-      }
-      if (t == 0 && ((kNeedMax && !(amax * rstd < kInf)) || (kNeedSum && !(sum < kInf)))) flag(p);
-    }
-    const RowScale r = row_scale<OUT>(amax, rstd);
-    if (kNeedMax && t == 0) p.scales[row] = stored_scale<OUT>(amax * rstd);
-#pragma unroll 2
-    for (int c = t; c < (chunks + 31 & ~31); c += T) {  // a warp's lanes stay together
-      Chunk y{};
-      f2 none = 0;
-      if (c < chunks) {
-        if constexpr (kNeedMax || kNeedSum)
-          y = kept(c);
-        else
-          y = first_values(c, none);
-      }
-      if (r.pre != 1.0f) y.scale(r.pre);
-      encode_chunk<SRC, OUT>(p, at, c, c < chunks, r, y, max_abs(y));
-    }
-    // the row's place in the ring is free: its next row
-    if constexpr (SRC != kSrcPlain && (kNeedMax || kNeedSum)) fence_proxy_async_smem();
-    __syncthreads();
-    if (t == 0 && row + shape.depth * step < p.rows) load(row + shape.depth * step, s);
-    if (++s == shape.depth) s = 0, phase ^= 1u;
-  }
-  // rows past the matrix in its last band of 128: zero scales
-  if constexpr (OUT != kOutE4M3)
-    for (int64_t row = p.rows + blockIdx.x; row < (p.rows + 127) / 128 * 128; row += step)
-      for (int k = t; k < tiles; k += T)
-        *reinterpret_cast<uint32_t *>(p.blocks + block_scale_offset(row, 4 * static_cast<int64_t>(k), tiles)) = 0u;
-}
-
 template <typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, unsigned threads, uint32_t smem, cudaStream_t st,
                              Args... args) {
@@ -638,41 +493,6 @@ cudaError_t launch_form(const RowQuantArgs &a, unsigned grid, unsigned threads, 
   return launch_dependent(rowquant_kernel<SRC, OUT, NC, WARP>, dim3(grid, segs, 1), threads, 0, st, a);
 }
 
-// The streamed form, where it has work for its CTAs and its rows fit; false
-// otherwise.
-template <int SRC, int OUT, int T>
-bool launch_stream(const RowQuantArgs &a, cudaStream_t st, cudaError_t &err) {
-  constexpr uint32_t kSm = 227 * 1024;
-  const uint64_t row = static_cast<uint64_t>(a.cols) * 2;
-  const uint64_t stage = row * (SRC == kSrcGate || a.residual ? 2 : 1), fixed = (SRC == kSrcNorm ? row : 0) + kStreamBars;
-  // CTAs an SM: as many as hold two rows each
-  uint64_t per = 1024 / T;
-  while (per > 1 && (2 * stage + fixed + 1280) * per > kSm) --per;
-  const uint64_t room = kSm / per - 1280;  // what the system and the reduction take of each
-  if (2 * stage + fixed > room) return false;
-  const uint64_t rounds = (a.rows + 148 * per - 1) / (148 * per);
-  uint64_t depth = (room - fixed) / stage;
-  depth = depth > 4 ? 4 : depth;
-  depth = depth > rounds ? rounds : depth;
-  const StreamShape sh{static_cast<int>(depth), static_cast<uint32_t>(stage)};
-  static std::atomic<uint64_t> ready{0};
-  err = allow_shared(stream_row_kernel<SRC, OUT, T>, 226 * 1024 - 512, ready);
-  if (err != cudaSuccess) return true;
-  const int64_t most = static_cast<int64_t>(148 * per), grid = a.rows < most ? a.rows : most;
-  err = launch_dependent(stream_row_kernel<SRC, OUT, T>, dim3(static_cast<unsigned>(grid)), T,
-                         static_cast<uint32_t>(fixed + depth * stage), st, a, sh);
-  return true;
-}
-
-// Times in us at 4096 rows with cold inputs, the norm (residual) to E4M3 / the
-// gate to E4M3 / the plain quantiser to nvfp4:
-//   columns      a CTA a row, 2 or 4 chunks a thread    streamed
-//   4096         21.6 / 16.6 / 14.2 (2 chunks)          24.0 / 17.1 / 15.7
-//   8192         41.7 / 31.6 / 28.0 (2)                 43.0 / 29.8 / 22.5
-//   14336        84.8 / 68.1 / 58.6 (4)                 66.1 / 50.4 / 38.3
-// A wide row's CTA is so large that two or three fill an SM, and loads and
-// arithmetic no longer overlap.  Four chunks a thread at 4096 columns: 23.3 /
-// 19.1 / 16.5.
 template <int SRC, int OUT>
 cudaError_t launch_out(const RowQuantArgs &a, cudaStream_t st) {
   const int64_t rows = OUT == kOutE4M3 ? a.rows : (a.rows + 127) / 128 * 128;
@@ -689,12 +509,11 @@ cudaError_t launch_out(const RowQuantArgs &a, cudaStream_t st) {
     const unsigned threads = static_cast<unsigned>((chunks + 32 * segs - 1) / (32 * segs) * 32);
     return launch_form<SRC, OUT, 1, false>(a, grid, threads, st, static_cast<unsigned>(segs));
   } else {
-    if (a.rows >= kStreamRows && chunks >= kStreamChunks) {
-      cudaError_t err;
-      if (chunks <= 576 ? launch_stream<SRC, OUT, 256>(a, st, err) : launch_stream<SRC, OUT, 512>(a, st, err)) return err;
-    }
     if (chunks > 2 * 1024) return launch_form<SRC, OUT, 0, false>(a, grid, 1024, st);
-    const int nc = chunks <= 512 || (chunks <= 1024 && a.rows <= kFewRows) ? 1 : 2;
+    // two chunks a thread above 8192 columns: 4096 x 14336 with 448 threads and
+    // not 896, norm to E4M3 64.8 against 79.6 us, quantiser to nvfp4 42 / 58;
+    // no difference at 8192
+    const int nc = chunks <= 512 ? 1 : 2;
     const unsigned threads = static_cast<unsigned>((chunks + 32 * nc - 1) / (32 * nc) * 32);
     if (nc == 1) return launch_form<SRC, OUT, 1, false>(a, grid, threads, st);
     return launch_form<SRC, OUT, 2, false>(a, grid, threads, st);
