@@ -479,6 +479,7 @@ int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const
  * activations, §2 "Pipeline de Implementacion").
  *   h = bf16(X + residual), or X when residual is NULL;
  *   y = h * rsqrt(mean(h^2) + eps) * weight, fp32, the mean over the row.
+ * host_eps points to eps in HOST memory (it is read before the call returns).
  * residual_out <- h (bf16 [rows, cols]; it may be X or residual itself, and
  * is NULL exactly when residual is).  weight bf16 [cols].
  * fp8_...: scales[m] = max(amax|y[m, :]| / 448, 2^-126) (1 for an all-zero
@@ -491,10 +492,10 @@ int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const
  * that row alone are unspecified.
  * SP24_ERR_SHAPE also for an eps that is negative or not finite.
  */
-int fp8_rmsnorm_quantize_pertoken(const void *X, const void *residual, const void *weight, float eps, int64_t rows,
-                                  int64_t cols, void *residual_out, uint8_t *q, float *scales, int32_t *status,
+int fp8_rmsnorm_quantize_pertoken(const void *X, const void *residual, const void *weight, const float *host_eps,
+                                  int64_t rows, int64_t cols, void *residual_out, uint8_t *q, float *scales, int32_t *status,
                                   sp24_stream_t stream);
-int fp4_rmsnorm_quantize_microscaled(const void *X, const void *residual, const void *weight, float eps,
+int fp4_rmsnorm_quantize_microscaled(const void *X, const void *residual, const void *weight, const float *host_eps,
                                      int64_t rows, int64_t cols, int format, void *residual_out, uint8_t *q,
                                      uint8_t *block_scales, float *row_scales, int32_t *status,
                                      sp24_stream_t stream);

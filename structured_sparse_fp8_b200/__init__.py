@@ -19,6 +19,8 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
+from ctypes import byref, c_float
+
 import torch
 
 from . import _lib
@@ -803,7 +805,7 @@ def fp8_rmsnorm_quantize_pertoken(X: torch.Tensor, weight: torch.Tensor, eps: fl
     supply q and scales."""
     rows, cols, dev, wp, rp, hp, h = _norm_inputs(X, weight, residual, residual_out)
     q, scales, qp, sp = _fp8_outputs(X, rows, cols, dev, out)
-    _call("fp8_rmsnorm_quantize_pertoken", dev, X.data_ptr(), rp, wp, eps, rows, cols, hp, qp, sp,
+    _call("fp8_rmsnorm_quantize_pertoken", dev, X.data_ptr(), rp, wp, byref(c_float(eps)), rows, cols, hp, qp, sp,
           _row_status(status, dev))
     return q, scales, h
 
@@ -818,7 +820,7 @@ def fp4_rmsnorm_quantize_microscaled(X: torch.Tensor, weight: torch.Tensor, eps:
     fmt = _fp4_format(format)
     rows, cols, dev, wp, rp, hp, h = _norm_inputs(X, weight, residual, residual_out)
     res, qp, bp, sp = _fp4_outputs(X, rows, cols, fmt, dev, out)
-    _call("fp4_rmsnorm_quantize_microscaled", dev, X.data_ptr(), rp, wp, eps, rows, cols, fmt[0], hp, qp, bp, sp,
+    _call("fp4_rmsnorm_quantize_microscaled", dev, X.data_ptr(), rp, wp, byref(c_float(eps)), rows, cols, fmt[0], hp, qp, bp, sp,
           _row_status(status, dev))
     return *res, h
 

@@ -33,7 +33,6 @@ _p = ctypes.c_void_p
 _i = ctypes.c_int
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
-_f = ctypes.c_float
 
 SIGNATURES = {
     "sp24_prune_compress": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _p, _sz, _p, _p]),
@@ -64,8 +63,8 @@ SIGNATURES = {
     "fp4_quantize_microscaled": (_i, [_p, _i64, _i64, _i, _p, _p, _p, _p, _p]),
     "fp4_unpack_e4m3": (_i, [_p, _i64, _i64, _p, _p]),
     "fp4_gemm_microscaled": (_i, [_p, _p, _p, _i, _p, _p, _p, _i, _i, _p, _i, _i, _i, _p, _p]),
-    "fp8_rmsnorm_quantize_pertoken": (_i, [_p, _p, _p, _f, _i64, _i64, _p, _p, _p, _p, _p]),
-    "fp4_rmsnorm_quantize_microscaled": (_i, [_p, _p, _p, _f, _i64, _i64, _i, _p, _p, _p, _p, _p, _p]),
+    "fp8_rmsnorm_quantize_pertoken": (_i, [_p, _p, _p, _p, _i64, _i64, _p, _p, _p, _p, _p]),
+    "fp4_rmsnorm_quantize_microscaled": (_i, [_p, _p, _p, _p, _i64, _i64, _i, _p, _p, _p, _p, _p, _p]),
     "fp8_silu_mul_quantize_pertoken": (_i, [_p, _i64, _i64, _p, _p, _p, _p]),
     "fp4_silu_mul_quantize_microscaled": (_i, [_p, _i64, _i64, _i, _p, _p, _p, _p, _p]),
     "sp24_workspace_size": (_sz, [_i, _i64, _i64, _i64, _i]),

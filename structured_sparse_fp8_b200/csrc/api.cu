@@ -578,27 +578,29 @@ int fp4_unpack_e4m3(const uint8_t *q, int64_t rows, int64_t cols, uint8_t *out, 
   return cuda_status(sp24::launch_fp4_unpack(q, rows * (cols / 2), out, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int fp8_rmsnorm_quantize_pertoken(const void *X, const void *residual, const void *weight, float eps, int64_t rows,
-                                  int64_t cols, void *residual_out, uint8_t *q, float *scales, int32_t *status,
+int fp8_rmsnorm_quantize_pertoken(const void *X, const void *residual, const void *weight, const float *host_eps,
+                                  int64_t rows, int64_t cols, void *residual_out, uint8_t *q, float *scales, int32_t *status,
                                   sp24_stream_t stream) {
+  if (!host_eps) return SP24_ERR_NULL;
   sp24::RowQuantArgs a = rowquant_args(X, rows, cols, q, nullptr, scales, status);
   a.residual = static_cast<const uint16_t *>(residual);
   a.weight = static_cast<const uint16_t *>(weight);
   a.residual_out = static_cast<uint16_t *>(residual_out);
-  a.eps = eps;
+  a.eps = *host_eps;
   return rowquant_common(kStageNorm, -1, a, stream);
 }
 
-int fp4_rmsnorm_quantize_microscaled(const void *X, const void *residual, const void *weight, float eps,
+int fp4_rmsnorm_quantize_microscaled(const void *X, const void *residual, const void *weight, const float *host_eps,
                                      int64_t rows, int64_t cols, int format, void *residual_out, uint8_t *q,
                                      uint8_t *block_scales, float *row_scales, int32_t *status,
                                      sp24_stream_t stream) {
   if (format < 0) return SP24_ERR_DTYPE;
+  if (!host_eps) return SP24_ERR_NULL;
   sp24::RowQuantArgs a = rowquant_args(X, rows, cols, q, block_scales, row_scales, status);
   a.residual = static_cast<const uint16_t *>(residual);
   a.weight = static_cast<const uint16_t *>(weight);
   a.residual_out = static_cast<uint16_t *>(residual_out);
-  a.eps = eps;
+  a.eps = *host_eps;
   return rowquant_common(kStageNorm, format, a, stream);
 }
 

@@ -843,11 +843,13 @@ cudaError_t launch_block(const MicroGemmArgs &a, cudaStream_t st) {
   if (a.M <= 16) return launch_narrow<BLOCK, 16>(a, p, st);
   if (a.M <= 32) return launch_narrow<BLOCK, 32>(a, p, st);
   // More than 64 tokens: narrow tiles as long as two or more slices of K fit
-  // (nvfp4, cold: 256 x 4096 x 4096, 128 tiles, 9.2 us against 11.7 on SM
-  // pairs; 384 x 4096 x 4096, 192 tiles, 12.2 against 10.6; 256 x 4096 x 512
-  // 5.6 against 4.9).
+  // and an SM gets 32 stages of them at most (nvfp4, cold, narrow / SM pairs:
+  // 256 x 4096 x 4096, 128 tiles of 16 stages, 9.2 / 11.7 us; 128 x 4096 x
+  // 14336, 64 of 56, 13.2 / 16.3; 256 x 4096 x 8192, 128 of 32, 12.5 / 13.4; 192
+  // x 4096 x 14336, 96 of 56, 17.6 / 16.3; 384 x 4096 x 4096, 192 of 16, 12.2 /
+  // 10.6).
   const int64_t tiles = static_cast<int64_t>((a.N + 127) / 128) * ((a.M + 63) / 64);
-  if (a.M <= 64 || tiles <= kNarrowTiles) return launch_narrow<BLOCK, 64>(a, p, st);
+  if (a.M <= 64 || (tiles <= kNarrowTiles && tiles * p.stages <= 32 * 148)) return launch_narrow<BLOCK, 64>(a, p, st);
   return launch_wide<BLOCK>(a, p, st);
 }
 

@@ -103,24 +103,27 @@ def test_quantize_refusals(lib):
 
 
 def test_norm_and_gate_refusals(lib):
+    EPS = ctypes.byref(ctypes.c_float(0.1))
     n8, n4 = lib.fp8_rmsnorm_quantize_pertoken, lib.fp4_rmsnorm_quantize_microscaled
     g8, g4 = lib.fp8_silu_mul_quantize_pertoken, lib.fp4_silu_mul_quantize_microscaled
-    assert n8(None, None, FAKE, 0.1, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL
-    assert n8(FAKE, None, None, 0.1, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL
-    assert n8(FAKE, FAKE, FAKE, 0.1, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL  # no residual_out
-    assert n8(FAKE, None, FAKE, 0.1, 4, 64, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL  # no residual
-    assert n8(FAKE, None, FAKE, 0.1, 4, 64, None, FAKE, None, None, None) == _lib.SP24_ERR_NULL
+    assert n8(None, None, FAKE, EPS, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL
+    assert n8(FAKE, None, None, EPS, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL
+    assert n8(FAKE, FAKE, FAKE, EPS, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL  # no residual_out
+    assert n8(FAKE, None, FAKE, EPS, 4, 64, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL  # no residual
+    assert n8(FAKE, None, FAKE, EPS, 4, 64, None, FAKE, None, None, None) == _lib.SP24_ERR_NULL
+    assert n8(FAKE, None, FAKE, None, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL
+    assert n4(FAKE, None, FAKE, None, 4, 64, 0, None, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_NULL
     for eps in (-1e-6, float("nan"), float("inf")):
-        assert n8(FAKE, None, FAKE, eps, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_SHAPE
-    assert n8(FAKE, None, FAKE, 0.1, 4, 40, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_SHAPE
-    assert n8(FAKE, None, FAKE, 0.1, 0, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_SHAPE
-    assert n8(FAKE, ODD, FAKE, 0.1, 4, 64, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_ALIGN
-    assert n8(FAKE, FAKE, FAKE, 0.1, 4, 64, ODD, FAKE, FAKE, None, None) == _lib.SP24_ERR_ALIGN
-    assert n8(FAKE, None, ODD, 0.1, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_ALIGN
-    assert n4(FAKE, None, FAKE, 0.1, 4, 64, 7, None, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_DTYPE
-    assert n4(FAKE, None, FAKE, 0.1, 4, 64, -1, None, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_DTYPE
-    assert n4(FAKE, None, FAKE, 0.1, 4, 64, 0, None, FAKE, None, FAKE, None, None) == _lib.SP24_ERR_NULL
-    assert n4(FAKE, None, FAKE, 0.1, 4, 48, 0, None, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_SHAPE
+        assert n8(FAKE, None, FAKE, ctypes.byref(ctypes.c_float(eps)), 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_SHAPE
+    assert n8(FAKE, None, FAKE, EPS, 4, 40, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_SHAPE
+    assert n8(FAKE, None, FAKE, EPS, 0, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_SHAPE
+    assert n8(FAKE, ODD, FAKE, EPS, 4, 64, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_ALIGN
+    assert n8(FAKE, FAKE, FAKE, EPS, 4, 64, ODD, FAKE, FAKE, None, None) == _lib.SP24_ERR_ALIGN
+    assert n8(FAKE, None, ODD, EPS, 4, 64, None, FAKE, FAKE, None, None) == _lib.SP24_ERR_ALIGN
+    assert n4(FAKE, None, FAKE, EPS, 4, 64, 7, None, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_DTYPE
+    assert n4(FAKE, None, FAKE, EPS, 4, 64, -1, None, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_DTYPE
+    assert n4(FAKE, None, FAKE, EPS, 4, 64, 0, None, FAKE, None, FAKE, None, None) == _lib.SP24_ERR_NULL
+    assert n4(FAKE, None, FAKE, EPS, 4, 48, 0, None, FAKE, FAKE, FAKE, None, None) == _lib.SP24_ERR_SHAPE
     assert g8(FAKE, 4, 24, FAKE, FAKE, None, None) == _lib.SP24_ERR_SHAPE
     assert g8(FAKE, 4, 32, None, FAKE, None, None) == _lib.SP24_ERR_NULL
     assert g8(ODD, 4, 32, FAKE, FAKE, None, None) == _lib.SP24_ERR_ALIGN
