@@ -483,8 +483,11 @@ int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const
  * residual_out <- h (bf16 [rows, cols]; it may be X or residual itself, and
  * is NULL exactly when residual is).  weight bf16 [cols].
  * fp8_...: scales[m] = max(amax|y[m, :]| / 448, 2^-126) (1 for an all-zero
- *   row), q u8 [rows, cols] = E4M3(y / scales[m]): an operand of
- *   sp24_gemm_packed_scaled.  cols % 16 == 0.
+ *   row), q u8 [rows, cols] = E4M3(y / scales[m]): the activations (Xq) of
+ *   sp24_gemm_packed_scaled.  cols % 16 == 0.  (As every activation stage of
+ *   this library it lets the next kernel start early, and fp8_gemm_dense loads
+ *   its Wq before it waits: q may be Wq of a call that is not the very next
+ *   one on the stream.)
  * fp4_...: y quantised as fp4_quantize_microscaled quantises (cols % 32 == 0).
  * No workspace.  Squares are summed in fp32 (a magnitude below about 1e-22
  * adds nothing).  SP24_STATUS_NONFINITE when a row holds NaN/Inf, or when its
@@ -504,8 +507,8 @@ int fp4_rmsnorm_quantize_microscaled(const void *X, const void *residual, const 
  * The gated activation between the two products of a feed-forward block, with
  * a quantised output.  GU bf16 [rows, 2 cols] holds the gate's columns, then
  * the up projection's (one GEMM over both weights stacked); y = g / (1 +
- * exp(-g)) * u in fp32, quantised as by the norm's two forms.  Shape rules,
- * status and outputs as there.
+ * exp(-g)) * u in fp32 (1 / (1 + exp(-g)) below 2^-130 counts as 0), quantised
+ * as by the norm's two forms.  Shape rules, status and outputs as there.
  */
 int fp8_silu_mul_quantize_pertoken(const void *GU, int64_t rows, int64_t cols, uint8_t *q, float *scales,
                                    int32_t *status, sp24_stream_t stream);

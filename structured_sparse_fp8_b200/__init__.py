@@ -664,8 +664,8 @@ def _tiles_size(rows, cols, block):
 
 
 def fp4_block_scales_size(rows: int, cols: int, format: str = "nvfp4") -> int:
-    """Bytes of the block-scale tiles of a [rows, cols] matrix."""
-    return _tiles_size(rows, cols, _fp4_format(format)[1])
+    """Bytes of the block-scale tiles of a [rows, cols] matrix (0 where there is none)."""
+    return _lib.load().fp4_block_scales_size(rows, cols, _fp4_format(format)[0])
 
 
 def _fp4_outputs(X, rows, cols, fmt, index, out):

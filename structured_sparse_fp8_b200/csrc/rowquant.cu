@@ -39,7 +39,6 @@
 
 #include "micro_common.cuh"
 #include "micro_kernels.h"
-#include "quant_common.cuh"
 #include "sm100_ptx.cuh"
 #include "sp24.h"
 
@@ -200,18 +199,21 @@ __device__ __forceinline__ Chunk norm_values(const Raw &h, const Raw &w, f2 &sum
   return y;
 }
 
-// g / (1 + exp(-g)) * u.  Where exp(-g) leaves fp32's range its reciprocal is 0.
+// g / (1 + exp(-g)) * u.  The reciprocal is taken of (1 + exp(-g)) / 16, so that
+// neither leaves the range of normal numbers while the factor is at least
+// 2^-130 (below that, from g = -90.1 on, it counts as 0): u may be large.
 __device__ __forceinline__ Chunk gate_values(const Raw &gv, const Raw &uv) {
   Chunk g = unpack(gv);
   const Chunk u = unpack(uv);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float2 a = split2(mul2(g.v[i], both(-1.4426950408889634f)));
+    const float2 a = split2(fma2(g.v[i], both(-1.4426950408889634f), both(-4.0f)));
     float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(a.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(a.y));
-    const float2 d = split2(add2(pack2(e.x, e.y), both(1.0f)));
-    g.v[i] = mul2(mul2(g.v[i], pack2(rcp_approx(d.x), rcp_approx(d.y))), u.v[i]);
+    const float2 d = split2(add2(pack2(e.x, e.y), both(0.0625f)));
+    const f2 sigmoid = mul2(pack2(rcp_approx(d.x), rcp_approx(d.y)), both(0.0625f));
+    g.v[i] = mul2(mul2(g.v[i], sigmoid), u.v[i]);
   }
   return g;
 }

@@ -7,6 +7,11 @@ size d, so a code must lie between the codes of the reference value times
 (1 - d) and (1 + d) under the kernel's own scales, and the scales likewise.
 The product is held to half a bf16 step plus the fp32 accumulation's error.
 """
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -302,6 +307,28 @@ def test_gate(fmt, shape):
     # the sum and the products round once each
     g = np.abs(O.bf16_to_f32(gu)[:, :cols].astype(np.float64))
     d = (1.173 * g + 8) * 2 * U
+    st = status()
+    if fmt == "e4m3":
+        q, s = sp().fp8_silu_mul_quantize_pertoken(dev_bf16(gu), status=st)
+        check_e4m3(q, s, y, d)
+    else:
+        q, b, s = sp().fp4_silu_mul_quantize_microscaled(dev_bf16(gu), fmt, status=st)
+        check_fp4(q, b, s, y, d, fmt)
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("cols", [64, 4096, 40032])
+def test_gate_of_far_negative_gates_and_large_up(fmt, cols):
+    """Gates whose factor 1 / (1 + exp(-g)) is below 2^-126, and up values that
+    bring the product back to ordinary size."""
+    x = np.tile(np.float64([-86.0, -87.0, -88.0, -89.0]), cols // 4)
+    up = np.tile(np.float64([3e38, 1e38, -2e38, 3e38]), cols // 4)
+    gu = WL.to_bf16_bits(np.concatenate([x, up])[None])
+    y = MO.silu_mul(gu)
+    assert np.abs(y).min() > 1
+    # as in test_gate, and the factor (at least 2^-129) is rounded to a multiple of 2^-149
+    d = (1.173 * np.abs(x)[None] + 8) * 2 * U + 2.0 ** -21
     st = status()
     if fmt == "e4m3":
         q, s = sp().fp8_silu_mul_quantize_pertoken(dev_bf16(gu), status=st)
@@ -643,6 +670,64 @@ def test_capture_replay_and_two_graphs_at_once(m):
         torch.cuda.synchronize()
         for i, (g, x, r, y) in zip(pair, graphs):
             assert torch.equal(y, want[i])
+
+
+FIRST_CALLS_IN_A_CAPTURE = """
+import torch
+import structured_sparse_fp8_b200 as sp
+torch.manual_seed(1)
+w = torch.ones(1024, device="cuda", dtype=torch.bfloat16)
+x = {m: torch.randn(m, 1024, device="cuda").to(torch.bfloat16) for m in (1, 300, 1500)}
+big = torch.randn(2048, 1024, device="cuda").to(torch.bfloat16)
+
+def block(m):
+    wq = sp.fp4_quantize_microscaled(big)
+    y = sp.fp4_gemm_microscaled(*sp.fp4_rmsnorm_quantize_microscaled(x[m], w, 1e-5)[:3], *wq)
+    return sp.fp8_silu_mul_quantize_pertoken(y)[0]
+
+for m in x:
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = block(m)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, block(m)) and bool(got.any()), m
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """No call prepares anything that a capture does not allow."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_IN_A_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+def test_calls_from_two_threads():
+    """Two threads on streams of their own, from a process's point of view at once."""
+    torch.manual_seed(3)
+    w = sp().fp4_quantize_microscaled(torch.randn(768, 1024, device=DEV).to(torch.bfloat16))
+    xs = [torch.randn(m, 1024, device=DEV).to(torch.bfloat16) for m in (1, 300)]
+
+    def run(x):
+        return sp().fp4_gemm_microscaled(*sp().fp4_quantize_microscaled(x), *w)
+
+    want = [run(x) for x in xs]
+    torch.cuda.synchronize()
+    same = [False, False]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [run(xs[i]) for _ in range(50)]
+            torch.cuda.current_stream().synchronize()
+            same[i] = all(torch.equal(g, want[i]) for g in got)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == [True, True]
 
 
 def test_calls_on_two_streams_at_once_and_after_foreign_work():
