@@ -38,7 +38,9 @@ struct RowQuantArgs {
   float *scales;             // E4M3 and nvfp4: one per row
   int64_t rows, cols;
   int32_t *status;
-  bool wide;                 // x, residual and residual_out are 32-byte aligned (set by the launch)
+  // set by the launch
+  int chunks, tiles;  // of a row: chunks of 16 elements, tiles of block scales
+  bool wide;          // x, residual and residual_out are 32-byte aligned
 };
 
 cudaError_t launch_rowquant_plain(RowOut out, const RowQuantArgs &a, cudaStream_t st);

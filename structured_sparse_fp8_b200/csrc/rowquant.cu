@@ -175,6 +175,26 @@ __device__ __forceinline__ float max_abs(const Chunk &c) {
   return m;
 }
 
+__device__ __forceinline__ float max_abs(const Raw &r) {
+  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&r.w[0]));
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&r.w[i])));
+  return max_nan(__low2float(m), __high2float(m));
+}
+
+// What a thread holds of a chunk between the two passes: the values, or for
+// plain rows the bf16 words as they came (half the registers).
+template <int SRC>
+struct Held {
+  Chunk v;
+  __device__ __forceinline__ Chunk values() const { return v; }
+};
+template <>
+struct Held<kSrcPlain> {
+  Raw v;
+  __device__ __forceinline__ Chunk values() const { return unpack(v); }
+};
+
 // bf16(x + r): the sum of two bf16 values rounded once (fp32 holds every such
 // sum that is near a rounding boundary exactly)
 __device__ __forceinline__ Raw add_bf16(const Raw &x, const Raw &r) {
@@ -225,23 +245,24 @@ struct Row {
   uint8_t *q, *blocks;           // blocks: scale 0 of the row; tile i is 512 i bytes on
 };
 template <int SRC, int OUT>
-__device__ __forceinline__ Row row_of(const RowQuantArgs &p, int64_t row, int tiles) {
+__device__ __forceinline__ Row row_of(const RowQuantArgs &p, int row) {
   Row r;
-  r.x = p.x + row * p.cols * (SRC == kSrcGate ? 2 : 1);
-  r.residual = SRC == kSrcGate ? r.x + p.cols : p.residual ? p.residual + row * p.cols : nullptr;
-  r.h = p.residual_out + row * p.cols;
-  r.q = p.q + row * (OUT == kOutE4M3 ? p.cols : p.cols / 2);
-  r.blocks = p.blocks + block_scale_offset(row, 0, tiles);
+  const int64_t chunk = static_cast<int64_t>(row) * p.chunks;  // the row's first
+  r.x = p.x + chunk * (kChunk * (SRC == kSrcGate ? 2 : 1));
+  r.residual = SRC == kSrcGate ? r.x + p.chunks * kChunk : p.residual + chunk * kChunk;
+  r.h = p.residual_out + chunk * kChunk;
+  r.q = p.q + chunk * (OUT == kOutE4M3 ? kChunk : kChunk / 2);
+  r.blocks = p.blocks + block_scale_offset(row, 0, p.tiles);
   return r;
 }
 
 // What chunk `c` of the row contributes: y, or z = h * w for the norm (then
 // also its sum of squares; `first` adds the residual and stores h).
 template <int SRC>
-__device__ __forceinline__ Chunk chunk_values(const RowQuantArgs &p, const Row &row, int c, bool first, f2 &sum) {
+__device__ __forceinline__ Held<SRC> chunk_values(const RowQuantArgs &p, const Row &row, int c, bool first, f2 &sum) {
   const int at = c * kChunk;
   if constexpr (SRC == kSrcPlain) {
-    return unpack(ld_row(row.x + at, p.wide));
+    return {ld_row(row.x + at, p.wide)};
   } else if constexpr (SRC == kSrcNorm) {
     const uint4 *w = reinterpret_cast<const uint4 *>(p.weight) + 2 * c;
     const uint4 w0 = __ldg(w), w1 = __ldg(w + 1);
@@ -253,10 +274,10 @@ __device__ __forceinline__ Chunk chunk_values(const RowQuantArgs &p, const Row &
     } else {
       h = ld_row((p.residual ? row.h : row.x) + at, p.wide);
     }
-    return norm_values(h, raw_of(w0, w1), sum);
+    return {norm_values(h, raw_of(w0, w1), sum)};
   } else {
     const Raw g = ld_row(row.x + at, p.wide), u = ld_row(row.residual + at, p.wide);
-    return gate_values(g, u);
+    return {gate_values(g, u)};
   }
 }
 
@@ -395,32 +416,31 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
   const int threads = WARP ? 32 : static_cast<int>(blockDim.x);
   const int seg = kSegs ? static_cast<int>(blockIdx.y) : 0, segs = kSegs ? static_cast<int>(gridDim.y) : 1;
   const int t = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x) + seg * NC * threads;
-  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : static_cast<int64_t>(blockIdx.x);
-  const int chunks = static_cast<int>(p.cols / kChunk);
-  const int tiles = static_cast<int>(OUT == kOutNvfp4 ? (p.cols + 63) / 64 : (p.cols + 127) / 128);
+  const int row = static_cast<int>(WARP ? blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x);
+  const int chunks = p.chunks;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (row >= p.rows) {
+  if (row >= static_cast<int>(p.rows)) {
     // a row past the matrix in its last band of 128: zero scales
-    if (OUT != kOutE4M3 && row < (p.rows + 127) / 128 * 128)
-      for (int i = threadIdx.x % threads + seg * threads; i < tiles; i += threads * segs)
-        *reinterpret_cast<uint32_t *>(p.blocks + block_scale_offset(row, 4 * static_cast<int64_t>(i), tiles)) = 0u;
+    if (OUT != kOutE4M3 && row < (static_cast<int>(p.rows) + 127) / 128 * 128)
+      for (int i = threadIdx.x % threads + seg * threads; i < p.tiles; i += threads * segs)
+        *reinterpret_cast<uint32_t *>(p.blocks + block_scale_offset(row, 4 * static_cast<int64_t>(i), p.tiles)) = 0u;
     return;
   }
   // ---- first pass: values, sum of squares, largest magnitude
-  const Row at = row_of<SRC, OUT>(p, row, tiles);
-  Chunk y[kLive];
+  const Row at = row_of<SRC, OUT>(p, row);
+  Held<SRC> y[kLive];
   f2 sums = 0;
   float top[kLive], sum = 0.0f, amax = 0.0f;
-  auto take = [&](int c, Chunk &v, float &most) {
+  auto take = [&](int c, Held<SRC> &v, float &most) {
     v = chunk_values<SRC>(p, at, c, true, sums);
-    most = max_abs(v);
+    most = max_abs(v.v);
     if constexpr (kNeedMax) amax = max_nan(amax, most);
   };
   if constexpr (NC > 0) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      y[i] = Chunk{};
+      y[i] = Held<SRC>{};
       top[i] = 0.0f;
       if (t + i * threads < chunks) take(t + i * threads, y[i], top[i]);
     }
@@ -451,7 +471,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
     if ((kNeedMax && !(amax * rstd < kInf)) || (kNeedSum && !(sum < kInf))) flag(p);
   }
   // ---- second pass: codes
-  auto put = [&](int c, bool on, Chunk v, float most) {
+  auto put = [&](int c, bool on, const Held<SRC> &held, float most) {
+    Chunk v = held.values();
     if (r.pre != 1.0f) {
       most *= r.pre;
       v.scale(r.pre);
@@ -466,10 +487,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(
 #pragma unroll 2
     for (int c0 = t & ~31; c0 < chunks; c0 += threads) {
       const int c = c0 + (t & 31);
-      Chunk v{};
+      Held<SRC> v{};
       f2 none = 0;
       if (c < chunks) v = chunk_values<SRC>(p, at, c, false, none);
-      put(c, c < chunks, v, max_abs(v));
+      put(c, c < chunks, v, max_abs(v.v));
     }
   }
 }
@@ -498,7 +519,7 @@ cudaError_t launch_form(const RowQuantArgs &a, unsigned grid, unsigned threads, 
 template <int SRC, int OUT>
 cudaError_t launch_out(const RowQuantArgs &a, cudaStream_t st) {
   const int64_t rows = OUT == kOutE4M3 ? a.rows : (a.rows + 127) / 128 * 128;
-  const int64_t chunks = a.cols / kChunk;
+  const int chunks = a.chunks;
   if (chunks <= 64) {
     const unsigned grid = static_cast<unsigned>((rows + kWarpRows - 1) / kWarpRows);
     if (chunks <= 32) return launch_form<SRC, OUT, 1, true>(a, grid, 32 * kWarpRows, st);
@@ -507,7 +528,7 @@ cudaError_t launch_out(const RowQuantArgs &a, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(rows);
   if constexpr (OUT == kOutMxfp4 && SRC != kSrcNorm) {
     // nothing to reduce over the row: CTAs of up to 256 threads, a chunk each
-    const int64_t segs = (chunks + 255) / 256;
+    const int segs = (chunks + 255) / 256;
     const unsigned threads = static_cast<unsigned>((chunks + 32 * segs - 1) / (32 * segs) * 32);
     return launch_form<SRC, OUT, 1, false>(a, grid, threads, st, static_cast<unsigned>(segs));
   } else {
@@ -528,6 +549,8 @@ cudaError_t launch(RowOut out, RowQuantArgs a, cudaStream_t st) {
   const uintptr_t bases = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
                           reinterpret_cast<uintptr_t>(a.residual_out);
   a.wide = bases % 32 == 0;
+  a.chunks = static_cast<int>(a.cols / kChunk);
+  a.tiles = static_cast<int>(out == kOutNvfp4 ? (a.cols + 63) / 64 : (a.cols + 127) / 128);
   if (out == kOutNvfp4) return launch_out<SRC, kOutNvfp4>(a, st);
   if (out == kOutMxfp4) return launch_out<SRC, kOutMxfp4>(a, st);
   if constexpr (SRC == kSrcPlain)
