@@ -20,19 +20,21 @@
 // (exact in fp32), sum h^2 and amax|z| come from one pass over the row, and
 // rstd enters the row's scale only.
 //
-// Such stages read and write each element once and are bound by memory, and
-// next by instruction issue: a thread takes 16 elements at a time (a block of
-// nvfp4, half one of mxfp4, a 32-byte access), so that a block's scale is
-// worked out once, and calculates on packed pairs.  A row is held in registers
-// from its one read to its last write: a warp per row up to 1024 columns, a
-// CTA of as many warps as the row needs up to 32768, and beyond that a CTA
-// that reads the row again for the second pass.  (8 elements a thread: norm to
-// E4M3, 4096 x 4096, 21.4 us against 18.9; quantiser to nvfp4, 12288 x 4096,
-// 37 against 29.  Rows brought ahead into shared memory by bulk copies of CTAs
-// that stay: 43 us against 35 for the norm at 4096 x 8192, 66 against 65 at
-// 4096 x 14336.)  Measured with cold inputs: norm to E4M3, 4096 x 4096, 18.9 us
-// (6.2 TB/s), 1 x 4096 1.9 us; gate to mxfp4, 4096 x 14336, 42.7 us (6.2 TB/s);
-// quantiser to mxfp4, 12288 x 4096, 23.2 us (5.5 TB/s).
+// Such stages read and write each element once and are bound by memory, next
+// by how many rows an SM has in flight (registers) and by instruction issue: a
+// thread takes 16 elements at a time (a block of nvfp4, half one of mxfp4, a
+// 32-byte access), so that a block's scale is worked out once, and calculates
+// on packed pairs.  A row is held in registers from its one read to its last
+// write: a warp per row up to 1024 columns, a CTA of as many warps as the row
+// needs up to 32768, and beyond that a CTA that reads the row again for the
+// second pass.  (8 elements a thread: norm to E4M3, 4096 x 4096, 21.4 us
+// against 18.9.  Plain rows held as values, not as bf16 words: quantiser to
+// nvfp4, 12288 x 4096, 29.3 us against 23.9.  Rows brought ahead into shared
+// memory by bulk copies of CTAs that stay: norm 43 us against 35 at 4096 x
+// 8192.)  Measured with cold inputs, bytes read and written over the time:
+// norm to E4M3, 4096 x 4096, 18.9 us (6.2 TB/s), 1 x 4096 1.9 us; gate to
+// mxfp4, 4096 x 14336, 39.8 us (6.7 TB/s); quantiser, 12288 x 4096, to mxfp4
+// 20.2 us (6.3 TB/s), to nvfp4 23.9 (5.4).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -407,9 +409,10 @@ __device__ __forceinline__ void flag(const RowQuantArgs &p) {
 
 // NC: chunks a thread holds in registers; 0: the row is read twice.
 // WARP: a warp per row, else a CTA, or gridDim.y CTAs where nothing is summed
-// or compared over the row.
-template <int SRC, int OUT, int NC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) rowquant_kernel(const RowQuantArgs p) {
+// or compared over the row.  FULL: at most 32 registers a thread, so that an
+// SM's threads are all taken.
+template <int SRC, int OUT, int NC, bool WARP, bool FULL>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024, FULL ? 2 : 0) rowquant_kernel(const RowQuantArgs p) {
   constexpr int kLive = NC > 0 ? NC : 1;
   __shared__ float2 red[32];
   constexpr bool kNeedMax = OUT != kOutMxfp4, kNeedSum = SRC == kSrcNorm, kSegs = !WARP && NC > 0 && !kNeedMax && !kNeedSum;
@@ -511,9 +514,9 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, unsigned thread
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int SRC, int OUT, int NC, bool WARP>
+template <int SRC, int OUT, int NC, bool WARP, bool FULL = false>
 cudaError_t launch_form(const RowQuantArgs &a, unsigned grid, unsigned threads, cudaStream_t st, unsigned segs = 1) {
-  return launch_dependent(rowquant_kernel<SRC, OUT, NC, WARP>, dim3(grid, segs, 1), threads, 0, st, a);
+  return launch_dependent(rowquant_kernel<SRC, OUT, NC, WARP, FULL>, dim3(grid, segs, 1), threads, 0, st, a);
 }
 
 template <int SRC, int OUT>
@@ -532,14 +535,22 @@ cudaError_t launch_out(const RowQuantArgs &a, cudaStream_t st) {
     const unsigned threads = static_cast<unsigned>((chunks + 32 * segs - 1) / (32 * segs) * 32);
     return launch_form<SRC, OUT, 1, false>(a, grid, threads, st, static_cast<unsigned>(segs));
   } else {
-    if (chunks > 2 * 1024) return launch_form<SRC, OUT, 0, false>(a, grid, 1024, st);
-    // two chunks a thread above 8192 columns: 4096 x 14336 with 448 threads and
-    // not 896, norm to E4M3 64.8 against 79.6 us, quantiser to nvfp4 42 / 58;
-    // no difference at 8192
-    const int nc = chunks <= 512 ? 1 : 2;
+    // (2000 x 40000: gate to nvfp4 136 / 107 us with the registers limited, norm
+    // to E4M3 118 / 120)
+    if (chunks > 2 * 1024) return launch_form<SRC, OUT, 0, false, SRC == kSrcGate>(a, grid, 1024, st);
+    // Two chunks a thread above 16384 columns, for plain rows (whose chunks
+    // take half the registers) above 8192: quantiser to nvfp4 with two / one,
+    // 2000 x 11008, 14.8 / 16.2 us; gate to E4M3, 4096 x 14336, 51.9 / 44.2,
+    // norm to nvfp4 65.0 / 59.1.
+    const int nc = chunks <= (SRC == kSrcPlain ? 512 : 1024) ? 1 : 2;
     const unsigned threads = static_cast<unsigned>((chunks + 32 * nc - 1) / (32 * nc) * 32);
-    if (nc == 1) return launch_form<SRC, OUT, 1, false>(a, grid, threads, st);
-    return launch_form<SRC, OUT, 2, false>(a, grid, threads, st);
+    if (nc == 2) return launch_form<SRC, OUT, 2, false>(a, grid, threads, st);
+    // Norms with a residual of up to 8192 columns, which already move 6 TB/s,
+    // are better off with 38 registers than with 32 (to nvfp4, 4096 x 4096,
+    // 18.0 / 18.8 us; without a residual 13.4 / 12.6).
+    if constexpr (SRC == kSrcNorm && OUT != kOutMxfp4)
+      if (a.residual && chunks <= 512) return launch_form<SRC, OUT, 1, false>(a, grid, threads, st);
+    return launch_form<SRC, OUT, 1, false, true>(a, grid, threads, st);
   }
 }
 
