@@ -625,7 +625,8 @@ def _bf16_rows(t, name):
         raise Sp24Error(f"{name} must be a 2-D bf16 tensor")
     if not t.is_cuda or not t.is_contiguous():
         raise Sp24Error("tensors must be contiguous CUDA tensors")
-    return t.size(0), t.size(1), t.get_device()
+    rows, cols = t.shape
+    return rows, cols, t.get_device()
 
 
 def _operand(t, name, dtype, numel, index):
@@ -677,7 +678,7 @@ def _fp4_outputs(X, rows, cols, fmt, index, out):
     if out:
         q, blocks, scales = out.get("q"), out.get("block_scales"), out.get("row_scales")
     if q is None:
-        q = X.new_empty((rows, cols // 2), dtype=_U8)
+        q = X.new_empty(rows, cols // 2, dtype=_U8)
         qp = q.data_ptr()
     else:
         qp = _operand(q, "q", _U8, rows * (cols // 2), index)
@@ -701,7 +702,7 @@ def _fp8_outputs(X, rows, cols, index, out):
     if out:
         q, scales = out.get("q"), out.get("scales")
     if q is None:
-        q = X.new_empty((rows, cols), dtype=_U8)
+        q = X.new_empty(rows, cols, dtype=_U8)
         qp = q.data_ptr()
     else:
         qp = _operand(q, "q", _U8, rows * cols, index)
@@ -734,9 +735,10 @@ def fp4_unpack_e4m3(q: torch.Tensor, out: torch.Tensor | None = None):
     if q.dtype != _U8 or q.dim() != 2:
         raise Sp24Error("q must be a 2-D uint8 tensor of packed FP4 codes")
     _require_cuda(q)
-    rows, cols, dev = q.size(0), 2 * q.size(1), q.get_device()
+    rows, half = q.shape
+    cols, dev = 2 * half, q.get_device()
     if out is None:
-        out = q.new_empty((rows, cols))
+        out = q.new_empty(rows, cols)
         op = out.data_ptr()
     else:
         op = _operand(out, "out", _U8, rows * cols, dev)
@@ -764,14 +766,15 @@ def fp4_gemm_microscaled(xq: torch.Tensor, x_block_scales: torch.Tensor, x_scale
     if xq.dtype != _U8 or xq.dim() != 2 or wq.dim() != 2:
         raise Sp24Error("xq and wq must be 2-D uint8 tensors of packed FP4 codes")
     _require_cuda(xq)
-    m, half, n, dev = xq.size(0), xq.size(1), wq.size(0), xq.get_device()
+    m, half = xq.shape
+    n, dev = wq.size(0), xq.get_device()
     wp = _operand(wq, "wq", _U8, n * half, dev)
     xb = _operand(x_block_scales, "x_block_scales", _U8, _tiles_size(m, 2 * half, block), dev)
     wb = _operand(w_block_scales, "w_block_scales", _U8, _tiles_size(n, 2 * half, block), dev)
     xs, x_vec = _row_scales(x_scales, "x_scales", m, dev)
     ws, w_vec = _row_scales(w_scales, "w_scales", n, dev)
     if out is None:
-        out = xq.new_empty((m, n), dtype=_BF16)
+        out = xq.new_empty(m, n, dtype=_BF16)
         yp = out.data_ptr()
     else:
         yp = _operand(out, "out", _BF16, m * n, dev)
