@@ -174,7 +174,7 @@ struct Narrow {
   // for BN = 16, held fewer bytes in flight: 1 x 11008 x 4096 7.5 us against
   // 7.2, 1 x 4096 x 14336 9.2 against 8.5.)
   static constexpr int kPerSm = 2;
-  static constexpr int kStages = (112 * 1024 - 3072 - (kOwnRoom ? kPartBytes : 0)) / kStageBytes;
+  static constexpr int kStages = (109 * 1024 - (kOwnRoom ? kPartBytes : 0)) / kStageBytes;
   // CTAs that a call is cut into, and stages of a slice at least
   static constexpr int kCtas = BN <= 16 ? 192 : 2 * kNarrowTiles;
   static constexpr int kSliceStages = BN <= 32 ? 3 : 4;
