@@ -631,12 +631,19 @@ def _bf16_rows(t, name):
 
 def _operand(t, name, dtype, numel, index):
     """Pointer of an input or output of a call: the right type and size,
-    contiguous, on the call's device."""
+    contiguous, on the call's device (a CPU tensor's index is -1)."""
     if t.dtype != dtype or t.numel() != numel:
         raise Sp24Error(f"{name} has the wrong shape or dtype")
-    if not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+    if t.get_device() != index or not t.is_contiguous():
         raise Sp24Error(f"{name} must be contiguous and on cuda:{index}")
     return t.data_ptr()
+
+
+def _matrix(t, name, dtype, rows, cols, index):
+    """The same of a matrix, whose shape must be the call's."""
+    if t.shape != (rows, cols):
+        raise Sp24Error(f"{name} must have shape ({rows}, {cols})")
+    return _operand(t, name, dtype, rows * cols, index)
 
 
 def _row_status(status, index):
@@ -681,7 +688,7 @@ def _fp4_outputs(X, rows, cols, fmt, index, out):
         q = X.new_empty(rows, cols // 2, dtype=_U8)
         qp = q.data_ptr()
     else:
-        qp = _operand(q, "q", _U8, rows * (cols // 2), index)
+        qp = _matrix(q, "q", _U8, rows, cols // 2, index)
     if blocks is None:
         blocks = X.new_empty(size, dtype=_U8)
         bp = blocks.data_ptr()
@@ -705,7 +712,7 @@ def _fp8_outputs(X, rows, cols, index, out):
         q = X.new_empty(rows, cols, dtype=_U8)
         qp = q.data_ptr()
     else:
-        qp = _operand(q, "q", _U8, rows * cols, index)
+        qp = _matrix(q, "q", _U8, rows, cols, index)
     if scales is None:
         scales = X.new_empty(rows, dtype=_F32)
         sp = scales.data_ptr()
@@ -741,7 +748,7 @@ def fp4_unpack_e4m3(q: torch.Tensor, out: torch.Tensor | None = None):
         out = q.new_empty(rows, cols)
         op = out.data_ptr()
     else:
-        op = _operand(out, "out", _U8, rows * cols, dev)
+        op = _matrix(out, "out", _U8, rows, cols, dev)
     _call("fp4_unpack_e4m3", dev, q.data_ptr(), rows, cols, op)
     return out
 
@@ -768,7 +775,7 @@ def fp4_gemm_microscaled(xq: torch.Tensor, x_block_scales: torch.Tensor, x_scale
     _require_cuda(xq)
     m, half = xq.shape
     n, dev = wq.size(0), xq.get_device()
-    wp = _operand(wq, "wq", _U8, n * half, dev)
+    wp = _matrix(wq, "wq", _U8, n, half, dev)
     xb = _operand(x_block_scales, "x_block_scales", _U8, _tiles_size(m, 2 * half, block), dev)
     wb = _operand(w_block_scales, "w_block_scales", _U8, _tiles_size(n, 2 * half, block), dev)
     xs, x_vec = _row_scales(x_scales, "x_scales", m, dev)
@@ -777,7 +784,7 @@ def fp4_gemm_microscaled(xq: torch.Tensor, x_block_scales: torch.Tensor, x_scale
         out = xq.new_empty(m, n, dtype=_BF16)
         yp = out.data_ptr()
     else:
-        yp = _operand(out, "out", _BF16, m * n, dev)
+        yp = _matrix(out, "out", _BF16, m, n, dev)
     _call("fp4_gemm_microscaled", dev, xq.data_ptr(), xb, xs, x_vec, wp, wb, ws, w_vec, code, yp, m, n, 2 * half,
           _row_status(status, dev))
     return out
@@ -790,12 +797,12 @@ def _norm_inputs(X, weight, residual, residual_out):
         if residual_out is not None:
             raise Sp24Error("residual_out needs a residual")
         return rows, cols, dev, wp, None, None, X
-    rp = _operand(residual, "residual", _BF16, rows * cols, dev)
+    rp = _matrix(residual, "residual", _BF16, rows, cols, dev)
     if residual_out is None:
         residual_out = torch.empty_like(X)
         hp = residual_out.data_ptr()
     else:
-        hp = _operand(residual_out, "residual_out", _BF16, rows * cols, dev)
+        hp = _matrix(residual_out, "residual_out", _BF16, rows, cols, dev)
     return rows, cols, dev, wp, rp, hp, residual_out
 
 

@@ -783,3 +783,21 @@ def test_python_refusals():
         m.fp4_gemm_microscaled(q, b, s, q, b, s, out=y)
     with pytest.raises(E):      # out is of another type
         m.fp4_gemm_microscaled(q, b, s, torch.cat([q, q]), b, None, out=torch.zeros(4, 8, device=DEV))
+
+
+def test_matrices_of_the_right_size_and_the_wrong_shape_are_refused():
+    m = sp()
+    x = torch.ones(4, 64, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(64, dtype=torch.bfloat16, device=DEV)
+    q, b, s = m.fp4_quantize_microscaled(x)
+    wq, wb, ws = m.fp4_quantize_microscaled(torch.ones(8, 64, dtype=torch.bfloat16, device=DEV))
+    for call in (lambda: m.fp8_rmsnorm_quantize_pertoken(x, w, 1e-5, residual=x.view(64, 4)),
+                 lambda: m.fp4_rmsnorm_quantize_microscaled(x, w, 1e-5, residual=x.view(8, 32)),
+                 lambda: m.fp4_rmsnorm_quantize_microscaled(x, w, 1e-5, residual=x, residual_out=torch.empty_like(x).view(-1)),
+                 lambda: m.fp4_quantize_microscaled(x, out=dict(q=q.view(8, 16))),
+                 lambda: m.fp8_silu_mul_quantize_pertoken(x, out=dict(q=torch.empty(8, 16, dtype=torch.uint8, device=DEV))),
+                 lambda: m.fp4_unpack_e4m3(q, out=torch.empty(8, 32, dtype=torch.uint8, device=DEV)),
+                 lambda: m.fp4_gemm_microscaled(q, b, s, wq, wb, ws, out=torch.empty(8, 4, dtype=torch.bfloat16, device=DEV)),
+                 lambda: m.fp4_gemm_microscaled(q, b, s, wq.view(16, 16), wb, ws)):
+        with pytest.raises(m.Sp24Error):
+            call()
