@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(Wide<BLOCK>::kThreads, 1)
     }
     mbar_init(&acc_full[0], 1);
     mbar_init(&acc_full[1], 1);
-    mbar_init(shared_free, 16);  // both CTAs' epilogue warps
+    mbar_init(shared_free, 8);  // both CTAs' epilogue warps of half 0
     mbar_init(arrived, 1);
     fence_mbar_init();
     mbar_arrive_expect_tx(arrived, (p.slices - 1) * (u1 - u0) * C::kUnitBytes);
@@ -551,14 +551,18 @@ __global__ void __launch_bounds__(Wide<BLOCK>::kThreads, 1)
     }
     __syncwarp();
   } else if (p.slices == 1) {
-    // The MMAs of tile j + 1 wait for all epilogue warps of both CTAs to
-    // arrive for tile j: the warps of the shared columns (half 0) once they
-    // hold tile j's, the others (half 1) once they have left tile j - 1, whose
-    // accumulator tile j + 1 takes.
+    // The MMAs of tile j + 1 wait for the warps of the shared columns (half 0)
+    // of both CTAs, which arrive once they hold tile j's.  Tile j - 1, whose
+    // accumulator tile j + 1 takes, has been left by then, by the other warps
+    // (half 1) too: half 0 passes tile j's first barrier only with them.  Half
+    // 1 must not arrive as well: it could be a tile ahead of the other CTA's
+    // half 0, and its arrival for tile j + 1 would stand in for the one that
+    // tile j still lacks.  Half 0 cannot be ahead, as it arrives for tile j + 1
+    // after that tile's products, which wait for tile j's arrivals.
     const int e = warp - 2, half = e >> 2, q = warp & 3;
     float *wsm = reinterpret_cast<float *>(smem + C::kWsOff);
     uint8_t *buf = smem + C::kYOff + e * C::kYBytes;
-    // one arrival a warp: 256 remote ones, a thread each, would queue
+    // one arrival a warp: a thread each, they would queue
     auto arrive = [&] {
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(shared_free, lead));
@@ -566,7 +570,6 @@ __global__ void __launch_bounds__(Wide<BLOCK>::kThreads, 1)
     int j = 0;
     for (int t = first; t < tiles; t += step, ++j) {
       const int mq = (t % p.tiles_m) * 256 + static_cast<int>(rank) * 128 + q * 32, n0 = (t / p.tiles_m) * 256;
-      if (half == 1) arrive();
       float xsm = 1.0f;
       if (p.xs) xsm = __ldg(p.xs + (p.x_vec ? min(mq + lane, p.M - 1) : 0));
       // the tile's weight scales, in the buffer of the tile before last

@@ -801,3 +801,29 @@ def test_matrices_of_the_right_size_and_the_wrong_shape_are_refused():
                  lambda: m.fp4_gemm_microscaled(q, b, s, wq.view(16, 16), wb, ws)):
         with pytest.raises(m.Sp24Error):
             call()
+
+
+def same_as_float64(y, xv, wv, xs, ws, band=2048):
+    """check_product of every value, in bands of rows."""
+    for i in range(0, y.shape[0], band):
+        check_product(y[i:i + band], xv[i:i + band], wv, xs[i:i + band], ws)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("m,n,k", [(8192, 16384, 64), (8192, 16384, 256), (5000, 24600, 128), (16384, 4104, 320)])
+def test_product_of_many_tiles_and_short_sums(fmt, m, n, k):
+    """Tens of tiles for each pair of SMs whose epilogues take longer than
+    their products: a tile's products must wait until both SMs have read the
+    accumulator columns that they reuse.  Every value, several times."""
+    xc, xb, xq, xt = operand(m, k, fmt, 9000 + k)
+    wc, wb, wq, wt = operand(n, k, fmt, 9100 + n)
+    g = torch.Generator(device=DEV).manual_seed(k)
+    xs, ws = torch.rand(m, device=DEV, generator=g) + 0.5, torch.rand(n, device=DEV, generator=g) + 0.5
+    st = status()
+    y = sp().fp4_gemm_microscaled(xq, xt, xs, wq, wt, ws, fmt, status=st)
+    same_as_float64(y, dev_values(xc, xb, fmt), dev_values(wc, wb, fmt), xs, ws)
+    out = torch.empty_like(y)
+    for _ in range(8):
+        out.fill_(7.0)
+        assert torch.equal(sp().fp4_gemm_microscaled(xq, xt, xs, wq, wt, ws, fmt, out=out, status=st), y)
+    assert int(st.item()) == 0
