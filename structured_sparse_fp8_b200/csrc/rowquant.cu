@@ -399,7 +399,9 @@ __device__ __forceinline__ void encode_chunk(const RowQuantArgs &p, const Row &r
     uint32_t word = on ? code << (8 * (lane / lanes & 3)) : 0u;
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, lanes);
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * lanes);
-    if (on && lane % (4 * lanes) == 0) *reinterpret_cast<uint32_t *>(row.blocks + c / (4 * lanes) * 512) = word;
+    // (tiles of a row of 2^28 columns and more pass 32-bit offsets)
+    if (on && lane % (4 * lanes) == 0)
+      *reinterpret_cast<uint32_t *>(row.blocks + static_cast<int64_t>(c / (4 * lanes)) * 512) = word;
   }
 }
 
@@ -408,8 +410,8 @@ __device__ __forceinline__ void flag(const RowQuantArgs &p) {
 }
 
 // NC: chunks a thread holds in registers; 0: the row is read twice.
-// WARP: a warp per row, else a CTA, or gridDim.y CTAs where nothing is summed
-// or compared over the row.  FULL: at most 32 registers a thread, so that an
+// WARP: a warp per row, else a CTA, or gridDim.y * gridDim.z CTAs where nothing
+// is summed or compared over the row.  FULL: at most 32 registers a thread, so that an
 // SM's threads are all taken.
 template <int SRC, int OUT, int NC, bool WARP, bool FULL>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024, FULL ? 2 : 0) rowquant_kernel(const RowQuantArgs p) {
@@ -417,7 +419,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024, FULL ? 2 : 0) ro
   __shared__ float2 red[32];
   constexpr bool kNeedMax = OUT != kOutMxfp4, kNeedSum = SRC == kSrcNorm, kSegs = !WARP && NC > 0 && !kNeedMax && !kNeedSum;
   const int threads = WARP ? 32 : static_cast<int>(blockDim.x);
-  const int seg = kSegs ? static_cast<int>(blockIdx.y) : 0, segs = kSegs ? static_cast<int>(gridDim.y) : 1;
+  const int seg = kSegs ? static_cast<int>(blockIdx.y + blockIdx.z * gridDim.y) : 0;
+  const int segs = kSegs ? static_cast<int>(gridDim.y * gridDim.z) : 1;
   const int t = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x) + seg * NC * threads;
   const int row = static_cast<int>(WARP ? blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x);
   const int chunks = p.chunks;
@@ -514,9 +517,14 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, unsigned thread
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+constexpr unsigned kMaxGridY = 65535;
+
 template <int SRC, int OUT, int NC, bool WARP, bool FULL = false>
 cudaError_t launch_form(const RowQuantArgs &a, unsigned grid, unsigned threads, cudaStream_t st, unsigned segs = 1) {
-  return launch_dependent(rowquant_kernel<SRC, OUT, NC, WARP, FULL>, dim3(grid, segs, 1), threads, 0, st, a);
+  // segments along y, past its limit along z too (then the last ones may lie
+  // behind the row, where they do nothing)
+  const unsigned z = (segs + kMaxGridY - 1) / kMaxGridY;
+  return launch_dependent(rowquant_kernel<SRC, OUT, NC, WARP, FULL>, dim3(grid, (segs + z - 1) / z, z), threads, 0, st, a);
 }
 
 template <int SRC, int OUT>

@@ -827,3 +827,63 @@ def test_product_of_many_tiles_and_short_sums(fmt, m, n, k):
         out.fill_(7.0)
         assert torch.equal(sp().fp4_gemm_microscaled(xq, xt, xs, wq, wt, ws, fmt, out=out, status=st), y)
     assert int(st.item()) == 0
+
+
+LONG = (1 << 28) + 65536 + 32     # columns past which scale offsets pass 2^31, and segments the grid's second axis
+
+
+def ends_of(blocks, q, lo, size, per_tile):
+    """Codes and scale tiles of the first and the last columns of a row of one band."""
+    return (q[:, :size // 2], blocks[:size // per_tile * 512]), (q[:, lo // 2:], blocks[lo // per_tile * 512:])
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("stage", ["plain", "gate"])
+def test_rows_of_2_to_28_columns(fmt, stage):
+    """The first and last columns of a very long row are quantised as in rows
+    of their own with the same largest value."""
+    per_tile, size = 4 * MO.BLOCK[fmt], 65536
+    lo = LONG // per_tile * per_tile - size
+    g = torch.Generator(device=DEV).manual_seed(5)
+
+    def made():
+        t = torch.randn(1, LONG, device=DEV, generator=g, dtype=torch.bfloat16)
+        t[0, 3] = t[0, lo + 7] = 20.0
+        return t
+
+    parts = [made() for _ in range(1 if stage == "plain" else 2)]
+    call = sp().fp4_quantize_microscaled if stage == "plain" else sp().fp4_silu_mul_quantize_microscaled
+    st = status()
+    q, b, s = call(torch.cat(parts, 1), fmt, status=st)
+    assert int(st.item()) == 0
+    for (gq, gb), cols in zip(ends_of(b, q, lo, size, per_tile), (slice(0, size), slice(lo, None))):
+        q1, b1, s1 = call(torch.cat([t[:, cols] for t in parts], 1), fmt)
+        assert torch.equal(gq, q1) and torch.equal(gb, b1) and (s is None or torch.equal(s, s1))
+
+
+@pytest.mark.parametrize("fmt,cols", [("nvfp4", LONG), ("mxfp4", 2 * LONG)])
+def test_norm_of_rows_of_2_to_28_columns(fmt, cols):
+    """A row and weights that repeat: so do the codes and the block scales."""
+    per_tile, period = 4 * MO.BLOCK[fmt], 65536
+    x = dev_bf16(WL.random_bits((1, period), 51)).repeat(1, cols // period + 1)[:, :cols].contiguous()
+    w = dev_bf16(WL.random_bits((1, period), 52)[0]).repeat(cols // period + 1)[:cols].contiguous()
+    st = status()
+    q, b, s, h = sp().fp4_rmsnorm_quantize_microscaled(x, w, 1e-5, fmt, status=st)
+    assert int(st.item()) == 0 and h is x
+    lo = cols // period * period
+    tail = cols - lo
+    assert torch.equal(q[:, lo // 2:], q[:, :tail // 2])
+    scales = b.view(-1, 512)[:, :4].reshape(-1)      # row 0 of each tile, blocks in order
+    n, first = tail // MO.BLOCK[fmt], lo // MO.BLOCK[fmt]
+    assert torch.equal(scales[first:first + n], scales[:n]) and bool(scales[:n].any())
+    whole = q[:, :lo // 2].view(-1, period // 2)
+    assert bool((whole == whole[:1]).all())
+    ws = scales[:first].view(-1, period // MO.BLOCK[fmt])
+    assert bool((ws == ws[:1]).all())
+    q1, b1, s1, _ = sp().fp4_rmsnorm_quantize_microscaled(x[:, :period].contiguous(), w[:period].contiguous(), 1e-5, fmt)
+    if fmt == "nvfp4":                               # without the root, which enters the row's scale only
+        assert torch.equal(q1, q[:, :period // 2]) and torch.equal(b1, b[:period // per_tile * 512])
+        # squares are added over 1024 threads of two lanes, cols / 2048 additions deep (the short row: 32), and the
+        # root halves their error; joining the threads, mean, root and scale are 20 roundings on either side; the
+        # last 32 columns weigh 32 * max(x)^2 / cols, which is below 2^-20 for |x| < 8
+        assert abs(s.item() / s1.item() - 1) < (cols / 4096 + 16 + 40) * U + 2.0 ** -20
