@@ -484,10 +484,8 @@ int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const
  * is NULL exactly when residual is).  weight bf16 [cols].
  * fp8_...: scales[m] = max(amax|y[m, :]| / 448, 2^-126) (1 for an all-zero
  *   row), q u8 [rows, cols] = E4M3(y / scales[m]): the activations (Xq) of
- *   sp24_gemm_packed_scaled.  cols % 16 == 0.  (As every activation stage of
- *   this library it lets the next kernel start early, and fp8_gemm_dense loads
- *   its Wq before it waits: q may be Wq of a call that is not the very next
- *   one on the stream.)
+ *   sp24_gemm_packed_scaled.  cols % 16 == 0.  (As Wq of fp8_gemm_dense: see
+ *   there.)
  * fp4_...: y quantised as fp4_quantize_microscaled quantises (cols % 32 == 0).
  * No workspace.  Squares are summed in fp32 (a magnitude below about 1e-22
  * adds nothing).  SP24_STATUS_NONFINITE when a row holds NaN/Inf, or when its
@@ -521,6 +519,14 @@ int fp4_silu_mul_quantize_microscaled(const void *GU, int64_t rows, int64_t cols
  * sparse speedup): Y[M, N] = bf16( x_scale * w_scale * sum_k Xq[m,k] Wq[n,k] )
  * with Xq u8 [M, K], Wq u8 [N, K] (E4M3, e.g. the pruned_dense output of
  * sp24_prune_compress).  Shape rules: M >= 1, N % 128 == 0, K % 128 == 0.
+ * Wq is read before the kernels ahead of this call are known to be complete.
+ * Codes that fp8_quantize_pertensor (or its static form), slide68_lift,
+ * fp8_rmsnorm_quantize_pertoken or fp8_silu_mul_quantize_pertoken wrote may be
+ * Wq only behind at least one more call on the stream that is not a GEMM of
+ * this library (the quantisation of X, for one), behind work of another
+ * library, or after the stream was synchronised: those stages let the next
+ * kernel start early, and the GEMMs pass that on.  What the other calls wrote
+ * may be Wq at once.
  */
 int fp8_gemm_dense(const uint8_t *Xq, const float *x_scale, const uint8_t *Wq,
                    const float *w_scale, void *Y, int M, int N, int K, void *workspace,

@@ -587,7 +587,15 @@ def sp24_gemm_packed_scaled(xq: torch.Tensor, x_scales: torch.Tensor, packed: to
 def fp8_gemm_dense(xq: torch.Tensor, x_scale, wq: torch.Tensor, w_scale,
                    out: torch.Tensor | None = None, status: torch.Tensor | None = None,
                    workspace: Workspace | None = None):
-    """Dense FP8 GEMM of the same kernel family (sparse-speedup baseline)."""
+    """Dense FP8 GEMM of the same kernel family (sparse-speedup baseline).
+
+    wq is read before the kernels ahead are known to be complete.  Codes of
+    fp8_quantize_pertensor, slide68_lift, fp8_rmsnorm_quantize_pertoken and
+    fp8_silu_mul_quantize_pertoken may be wq only behind one more call on the
+    stream that is not a GEMM of this library (such as the quantisation of X),
+    behind work of another library, or after a synchronisation; what other
+    calls wrote may be wq at once.
+    """
     lib = _lib.load()
     _require_cuda(xq, x_scale, wq, w_scale, out, status)
     M, K = xq.shape
@@ -812,7 +820,7 @@ def fp8_rmsnorm_quantize_pertoken(X: torch.Tensor, weight: torch.Tensor, eps: fl
     """Root-mean-square norm of h = X + residual with E4M3 output: returns (q u8
     [rows, cols], scales f32 [rows], h bf16 [rows, cols]); without a residual h
     is X itself.  residual_out may be X or residual (in place); ``out`` may
-    supply q and scales."""
+    supply q and scales.  q is for Xq of a GEMM (as wq: see fp8_gemm_dense)."""
     rows, cols, dev, wp, rp, hp, h = _norm_inputs(X, weight, residual, residual_out)
     q, scales, qp, sp = _fp8_outputs(X, rows, cols, dev, out)
     _call("fp8_rmsnorm_quantize_pertoken", dev, X.data_ptr(), rp, wp, byref(c_float(eps)), rows, cols, hp, qp, sp,
@@ -844,7 +852,8 @@ def _gated_rows(GU):
 
 def fp8_silu_mul_quantize_pertoken(GU: torch.Tensor, status: torch.Tensor | None = None, out: dict | None = None):
     """silu(gate) * up of GU bf16 [rows, 2 cols] (gate columns, then up columns)
-    with E4M3 output: returns (q u8 [rows, cols], scales f32 [rows])."""
+    with E4M3 output: returns (q u8 [rows, cols], scales f32 [rows]).  q is for
+    Xq of a GEMM (as wq: see fp8_gemm_dense)."""
     rows, cols, dev = _gated_rows(GU)
     q, scales, qp, sp = _fp8_outputs(GU, rows, cols, dev, out)
     _call("fp8_silu_mul_quantize_pertoken", dev, GU.data_ptr(), rows, cols, qp, sp, _row_status(status, dev))

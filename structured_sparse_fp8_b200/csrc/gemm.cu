@@ -561,7 +561,13 @@ __global__ void __launch_bounds__(Config<KIND, BN, MT, KB, XQ>::kThreads, Config
   // written by the weight-path kernels (prune/compress, decompose), which do
   // not release their dependents early, so the producer may stream weight
   // tiles right away; activations, scales and Y are touched only after
-  // griddepcontrol.wait, i.e. after the previous kernel has completed.
+  // griddepcontrol.wait, i.e. after the previous kernel has completed.  The
+  // producer's warp releases the next grid before that wait, so two grids can
+  // look ahead, and the dense form's weights must not come from an 8-bit
+  // activation stage with nothing but such grids in between (sp24.h states
+  // it).  Released by the waiting warps only, that use would be sound, but 1 x
+  // 11008 x 4096 behind its like takes 9.1 us for 8.5 (dense 13.0 for 11.0),
+  // fused 12.3 for 10.4.
   if (warp != 0) grid_dependency_wait();
   grid_launch_dependents();
 

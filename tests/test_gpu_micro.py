@@ -887,3 +887,53 @@ def test_norm_of_rows_of_2_to_28_columns(fmt, cols):
         # root halves their error; joining the threads, mean, root and scale are 20 roundings on either side; the
         # last 32 columns weigh 32 * max(x)^2 / cols, which is below 2^-20 for |x| < 8
         assert abs(s.item() / s1.item() - 1) < (cols / 4096 + 16 + 40) * U + 2.0 ** -20
+
+
+@pytest.mark.parametrize("stage", ["norm", "gate"])
+def test_codes_are_weights_behind_a_quantiser(stage):
+    """E4M3 codes of a row stage as the dense FP8 GEMM's weights, with the short
+    quantisation of X in between: the GEMM's early loads of weights must not
+    start while the stage still writes them."""
+    n, k = 4096, 2048
+    m = sp()
+    x8 = dev_bf16(WL.random_bits((8, k), 23))
+    xq, sx = m.fp8_quantize_pertensor(x8)
+    one = torch.ones(1, device=DEV)
+    w = dev_bf16(WL.random_bits((1, k), 24)[0])
+    ins = [torch.randn(n, k if stage == "norm" else 2 * k, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    out = dict(q=torch.empty(n, k, dtype=torch.uint8, device=DEV), scales=torch.empty(n, device=DEV))
+
+    def codes(x):
+        if stage == "norm":
+            m.fp8_rmsnorm_quantize_pertoken(x, w, 1e-5, out=out)
+        else:
+            m.fp8_silu_mul_quantize_pertoken(x, out=out)
+
+    want = []
+    for x in ins:
+        codes(x)
+        torch.cuda.synchronize()
+        want.append(m.fp8_gemm_dense(xq, sx, out["q"], one))
+        torch.cuda.synchronize()
+    assert not torch.equal(*want)
+    y = torch.empty_like(want[0])
+    ws = m.Workspace(DEV)
+    same = torch.ones((), dtype=torch.bool, device=DEV)
+
+    def run(i):
+        codes(ins[i])
+        a, sa = m.fp8_quantize_pertensor(x8, workspace=ws)
+        m.fp8_gemm_dense(a, sa, out["q"], one, out=y, workspace=ws)
+        same.logical_and_((y == want[i]).all())
+
+    graphs = []
+    for i in range(2):
+        run(i)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            run(i)
+    for i in range(100):
+        graphs[i % 2].replay()
+        run(i % 2)
+    assert bool(same)
