@@ -487,10 +487,12 @@ int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const
  *   sp24_gemm_packed_scaled.  cols % 16 == 0.  (As Wq of fp8_gemm_dense: see
  *   there.)
  * fp4_...: y quantised as fp4_quantize_microscaled quantises (cols % 32 == 0).
- * No workspace.  Squares are summed in fp32 (a magnitude below about 1e-22
- * adds nothing).  SP24_STATUS_NONFINITE when a row holds NaN/Inf, or when its
- * sum of squares or a product h * weight leaves fp32's range; the outputs of
- * that row alone are unspecified.
+ * No workspace.  Squares are summed in fp32: a magnitude below about 1e-22
+ * adds nothing and one below 1e-19 is squared with fewer bits, which shows only
+ * where eps is smaller still; y is 0 where the mean and eps are.
+ * SP24_STATUS_NONFINITE when a row holds NaN/Inf, or when its sum of squares, a
+ * product h * weight or a y leaves fp32's range; the outputs of that row alone
+ * are unspecified.
  * SP24_ERR_SHAPE also for an eps that is negative or not finite.
  */
 int fp8_rmsnorm_quantize_pertoken(const void *X, const void *residual, const void *weight, const float *host_eps,

@@ -308,10 +308,15 @@ __device__ __forceinline__ RowScale row_scale(float amax, float rstd) {
     if (amax >= 0x1p-64f && amax <= 0x1p100f && amax * rstd >= least) {
       r.sf = 448.0f * rcp_refined(amax);
     } else {
-      const float big = amax > 0x1p100f ? 0x1p-64f : 0x1p64f;
-      r.pre = big;
-      // (the row's values are multiplied by pre first)
-      const float R = amax * rstd >= least ? amax * big : rstd > 0.0f ? __fdiv_rn(least, rstd) * big : 1.0f;
+      // The row's values are multiplied by pre first, and R is scaled by it
+      // before the division, which may leave fp32's range otherwise: amax is
+      // at least 2^-149, so this R is at least 2^-86.
+      r.pre = amax > 0x1p100f ? 0x1p-64f : 0x1p64f;
+      float R = kInf;  // a row of zeros, or one whose squares all vanish: zero codes
+      if (amax * rstd >= least)
+        R = amax * r.pre;
+      else if (amax > 0.0f && rstd > 0.0f)
+        R = __fdiv_rn(least * r.pre, rstd);
       r.sf = __fdiv_rn(448.0f, R);
     }
     r.mul = OUT == kOutE4M3 ? r.sf : 6.0f * r.sf;

@@ -937,3 +937,61 @@ def test_codes_are_weights_behind_a_quantiser(stage):
         graphs[i % 2].replay()
         run(i % 2)
     assert bool(same)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("cols", [64, 4096, 40032])
+@pytest.mark.parametrize("size", [1e-4, 1e-10, 1e-12, 1e-19, 1e-20, 1e-25, 1e-38])
+def test_norm_of_small_rows_whose_products_are_zero(fmt, cols, size):
+    """Without eps, rows that are small but not zero under weights that are zero
+    wherever the row is not: zero codes, the scale 1, no status."""
+    x, w = np.zeros((2, cols)), np.ones(cols)
+    x[0, ::2], x[1, 5] = -size, size
+    w[::2], w[5] = 0.0, 0.0
+    X, W, st = dev_bf16(WL.to_bf16_bits(x)), dev_bf16(WL.to_bf16_bits(w)), status()
+    if fmt == "e4m3":
+        q, s, _ = sp().fp8_rmsnorm_quantize_pertoken(X, W, 0.0, status=st)
+    else:
+        q, b, s, _ = sp().fp4_rmsnorm_quantize_microscaled(X, W, 0.0, fmt, status=st)
+        assert not b.any()
+        q = torch.from_numpy(unpack(q) & 7)
+    assert not (q & 0x7F).any() and (s is None or s.tolist() == [1.0, 1.0]) and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("cols", [96, 4096, 40032])
+def test_norm_of_rows_whose_squares_vanish(fmt, cols):
+    """Without eps, a row whose mean square is 0 in fp32 is a row of zeros,
+    under weights of any size."""
+    x, w = np.full((2, cols), 2.0 ** -80), np.full(cols, 2.0 ** 120)
+    x[1] = 1.0
+    st = status()
+    X, W = dev_bf16(WL.to_bf16_bits(x)), dev_bf16(WL.to_bf16_bits(w))
+    if fmt == "e4m3":
+        q, s, _ = sp().fp8_rmsnorm_quantize_pertoken(X, W, 0.0, status=st)
+    else:
+        q, _, s, _ = sp().fp4_rmsnorm_quantize_microscaled(X, W, 0.0, fmt, status=st)
+    assert not q[0].any() and bool(q[1].all()) and (s is None or s[0].item() == 1.0) and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("fmt,size,weight", [("e4m3", 2.0 ** -12, 2.0 ** -121), ("e4m3", 2.0 ** 40, 2.0 ** -122),
+                                             ("nvfp4", 2.0 ** -30, 2.0 ** -93), ("nvfp4", 2.0 ** 50, 2.0 ** -95)])
+@pytest.mark.parametrize("cols", [96, 4096, 40032])
+def test_norm_of_rows_below_the_least_scale(fmt, size, weight, cols):
+    """Rows whose largest value is below what the least row scale stands for."""
+    x, w = WL.random_bits((3, cols), 31, scale=size), WL.random_bits((1, cols), 32, scale=weight)[0]
+    y, _ = MO.rmsnorm(x, None, w, 0.0)
+    # h * w is rounded to a multiple of 2^-149
+    z = np.abs(O.bf16_to_f32(x).astype(np.float64) * O.bf16_to_f32(w).astype(np.float64))
+    d = norm_error(cols) + np.where(z > 0, 2.0 ** -150 / np.where(z > 0, z, 1.0), 0.0)
+    assert np.abs(y).max() < (448.0 * 2.0 ** -126 if fmt == "e4m3" else MO.ROW_FLOOR)
+    X, W, st = dev_bf16(x), dev_bf16(w), status()
+    if fmt == "e4m3":
+        q, s, _ = sp().fp8_rmsnorm_quantize_pertoken(X, W, 0.0, status=st)
+        assert s.tolist() == [2.0 ** -126] * 3
+        check_e4m3(q, s, y, d)
+    else:
+        q, b, s, _ = sp().fp4_rmsnorm_quantize_microscaled(X, W, 0.0, fmt, status=st)
+        assert s.tolist() == [2.0 ** -100] * 3
+        check_fp4(q, b, s, y, d, fmt)
+    assert int(st.item()) == 0
