@@ -466,7 +466,8 @@ int fp4_unpack_e4m3(const uint8_t *q, int64_t rows, int64_t cols, uint8_t *out, 
  * matrix does not matter), of [M, K] and [N, K].  Products below 2^-126 may
  * count as zero.  Y bf16 [M, N] must not alias an
  * input.  No workspace; the same inputs give the same bits.  Shape rules:
- * 1 <= M <= 2^31 - 256, 8 <= N <= 2^31 - 256, N % 8 == 0, K >= 64, K % 64 == 0.
+ * 1 <= M <= 2^31 - 256, 8 <= N <= 2^31 - 256, N % 8 == 0, 64 <= K <= 2^31 -
+ * 256, K % 64 == 0.
  */
 int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const float *x_scales, int x_per_token,
                          const uint8_t *Wq, const uint8_t *w_block_scales, const float *w_scales, int w_per_channel,

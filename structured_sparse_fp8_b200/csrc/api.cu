@@ -622,8 +622,8 @@ int fp4_gemm_microscaled(const uint8_t *Xq, const uint8_t *x_block_scales, const
   const int block = fp4_block(format);
   if (!block) return SP24_ERR_DTYPE;
   if (!Xq || !x_block_scales || !Wq || !w_block_scales || !Y) return SP24_ERR_NULL;
-  constexpr int kMost = INT32_MAX - 255;  // a tile's last row stays an int
-  if (M < 1 || M > kMost || N < 8 || N > kMost || N % 8 != 0 || K < 64 || K % 64 != 0) return SP24_ERR_SHAPE;
+  constexpr int kMost = INT32_MAX - 255;  // a tile's last row and a stage's last column stay ints
+  if (M < 1 || M > kMost || N < 8 || N > kMost || N % 8 != 0 || K < 64 || K > kMost || K % 64 != 0) return SP24_ERR_SHAPE;
   if (!aligned16(Xq) || !aligned16(x_block_scales) || !aligned16(Wq) || !aligned16(w_block_scales) || !aligned16(Y) ||
       !aligned16(x_scales) || !aligned16(w_scales))
     return SP24_ERR_ALIGN;

@@ -995,3 +995,23 @@ def test_norm_of_rows_below_the_least_scale(fmt, size, weight, cols):
         assert s.tolist() == [2.0 ** -100] * 3
         check_fp4(q, b, s, y, d, fmt)
     assert int(st.item()) == 0
+
+
+def test_product_of_the_longest_sum():
+    """K at its limit: what lies at either end of the row arrives, alone."""
+    m, n, k, end = 1, 8, (1 << 31) - 256, 512
+    n_end, tile = end // 32, 512
+    xc, xb, xq, xt = operand(m, 2 * end, "mxfp4", 41)
+    wc, wb, wq, wt = operand(n, 2 * end, "mxfp4", 42)
+
+    def long(q, t, rows):
+        lq = torch.zeros(rows, k // 2, dtype=torch.uint8, device=DEV)
+        lt = torch.zeros(k // 128 * tile, dtype=torch.uint8, device=DEV)
+        for got, src, cut in ((lq, q, end // 2), (lt.view(1, -1), t.view(1, -1), n_end // 4 * tile)):
+            got[:, :cut], got[:, -cut:] = src[:, :cut], src[:, -cut:]
+        return lq, lt
+
+    (lxq, lxt), (lwq, lwt), st = long(xq, xt, m), long(wq, wt, n), status()
+    y = sp().fp4_gemm_microscaled(lxq, lxt, None, lwq, lwt, None, "mxfp4", status=st)
+    check_product(y, dev_values(xc, xb, "mxfp4"), dev_values(wc, wb, "mxfp4"), None, None)
+    assert int(st.item()) == 0 and bool(y.any())

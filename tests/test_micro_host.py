@@ -148,6 +148,14 @@ def test_gemm_refusals(lib):
         assert call(**bad) == _lib.SP24_ERR_SHAPE
 
 
+def test_gemm_refuses_sums_whose_stages_pass_an_int(lib):
+    g = lib.fp4_gemm_microscaled
+    for k in (1 << 31) - 64, (1 << 31) - 128, (1 << 31) - 192:
+        assert g(FAKE, FAKE, FAKE, 1, FAKE, FAKE, FAKE, 1, 0, FAKE, 1, 8, k, None, None) == _lib.SP24_ERR_SHAPE
+    # the longest sum passes the checks of shapes (and is refused for its alignment here)
+    assert g(ODD, FAKE, FAKE, 1, FAKE, FAKE, FAKE, 1, 0, FAKE, 1, 8, (1 << 31) - 256, None, None) == _lib.SP24_ERR_ALIGN
+
+
 # ------------------------------------------------------------------ Python
 def test_python_refuses_cpu_tensors_and_unknown_formats(lib):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
