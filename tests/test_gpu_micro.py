@@ -1015,3 +1015,75 @@ def test_product_of_the_longest_sum():
     y = sp().fp4_gemm_microscaled(lxq, lxt, None, lwq, lwt, None, "mxfp4", status=st)
     check_product(y, dev_values(xc, xb, "mxfp4"), dev_values(wc, wb, "mxfp4"), None, None)
     assert int(st.item()) == 0 and bool(y.any())
+
+
+@pytest.mark.parametrize("stage", ["nvfp4", "mxfp4", "norm e4m3", "norm nvfp4", "gate e4m3", "gate mxfp4", "unpack"])
+def test_last_rows_of_matrices_past_32_bit_offsets(stage):
+    """More than 2^31 elements (and 2^32 bytes in each input), whose last rows
+    are like no others: they come out as from a call of their own, and not as
+    rows that lie 2^31 elements or 2^32 bytes before them."""
+    rows, cols = 131200, 32768
+    lo = rows - 128
+    op, _, fmt = stage.partition(" ")
+    m, g = sp(), torch.Generator(device=DEV).manual_seed(7)
+
+    def made(width):
+        t = torch.randn(512, width, device=DEV, generator=g).to(torch.bfloat16).repeat(-(-rows // 512), 1)[:rows]
+        t[lo:] = torch.randn(rows - lo, width, device=DEV, generator=g).to(torch.bfloat16)
+        return t
+
+    if op == "norm":
+        ins = [made(cols)]
+        w = dev_bf16(WL.random_bits((1, cols), 8)[0])
+        if fmt == "e4m3":
+            ins.append(made(cols))
+            call = lambda x, r: m.fp8_rmsnorm_quantize_pertoken(x, w, 1e-5, residual=r)
+        else:
+            call = lambda x: m.fp4_rmsnorm_quantize_microscaled(x, w, 1e-5, fmt)[:3]
+    elif op == "gate":
+        ins = [made(2 * cols)]
+        call = m.fp8_silu_mul_quantize_pertoken if fmt == "e4m3" else lambda x: m.fp4_silu_mul_quantize_microscaled(x, fmt)
+    elif op == "unpack":
+        ins = [torch.randint(0, 256, (512, cols), device=DEV, generator=g, dtype=torch.uint8).repeat(-(-rows // 512), 1)[:rows]]
+        ins[0][lo:] = torch.randint(0, 256, (rows - lo, cols), device=DEV, generator=g, dtype=torch.uint8)
+        call = lambda x: (m.fp4_unpack_e4m3(x),)
+    else:
+        ins = [made(cols)]
+        call = lambda x: m.fp4_quantize_microscaled(x, op)
+    got = call(*ins)
+    want = call(*(t[lo:].contiguous() for t in ins))
+    other = call(*(t[lo - 65536:lo - 65536 + 128].contiguous() for t in ins))
+    assert not torch.equal(other[0], want[0])
+    for a, b in zip(got, want):
+        if a is not None:
+            # blocks' scales: the last band of 128 rows
+            assert torch.equal(a[-b.numel():] if a.dim() == 1 else a[lo:], b)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("n", [8, 256])
+def test_product_of_rows_past_32_bit_offsets(fmt, n):
+    """Codes of more than 2^31 bytes whose last rows are like no others."""
+    rows, cols = 131200, 32768 + 128
+    x = torch.randn(512, cols, device=DEV).to(torch.bfloat16)
+    x = x.repeat(-(-rows // 512), 1)[:rows]
+    x[-128:] = torch.randn(128, cols, device=DEV).to(torch.bfloat16)
+    q, b, s = sp().fp4_quantize_microscaled(x, fmt)
+    del x
+    assert q.numel() > 1 << 31
+    w = sp().fp4_quantize_microscaled(torch.randn(n, cols, device=DEV).to(torch.bfloat16), fmt)
+    size = b.numel() // (rows // 128)
+    wv = dev_values(unpack(w[0]), rows_of(w[1], n, cols, fmt), fmt)
+
+    def check(y, lo):
+        bt = b[lo // 128 * size:(lo // 128 + 1) * size]
+        xv = dev_values(unpack(q[lo:lo + 128]), rows_of(bt, 128, cols, fmt), fmt)
+        check_product(y, xv, wv, None if s is None else s[lo:lo + 128], w[2])
+
+    y = sp().fp4_gemm_microscaled(q, b, s, *w, fmt)
+    for lo in (0, 65536, rows - 256, rows - 128):
+        check(y[lo:lo + 128], lo)
+    # and as the weights
+    y = sp().fp4_gemm_microscaled(*w, q, b, s, fmt)
+    for lo in (0, 65536, rows - 256, rows - 128):
+        check(y[:, lo:lo + 128].t(), lo)
