@@ -39,7 +39,6 @@
 #include <stdint.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "kernels.h"
 #include "micro_common.cuh"
@@ -723,33 +722,27 @@ __global__ void __launch_bounds__(Wide<BLOCK>::kThreads, 1)
 
 // ------------------------------------------------------------------ host
 
-// Clusters of `slices` SM pairs of the wide kernel that a device runs at once
-// (148 SMs hold 74, 33 and 22); asked once, with the kernel's shared memory
+// Clusters of `slices` SM pairs of the wide kernel that the current device
+// runs at once (148 SMs hold 74, 33 and 22), with the kernel's shared memory
 // allowed.
 template <int BLOCK>
-int wide_clusters(int slices) {
-  static int cap[kMaxWideSlices + 1] = {};
-  static std::once_flag once;
-  std::call_once(once, [] {
-    for (unsigned i = 1; i <= kMaxWideSlices; ++i) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2 * i, 1, 1);
-      cfg.blockDim = dim3(Wide<BLOCK>::kThreads, 1, 1);
-      cfg.dynamicSmemBytes = Wide<BLOCK>::kSmem;
-      cudaLaunchAttribute at[1];
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = 2 * i;
-      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-      cfg.attrs = at;
-      cfg.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, wide_kernel<BLOCK>, &cfg) == cudaSuccess)
-        cap[i] = n;
-      else
-        (void)cudaGetLastError();
-    }
+cudaError_t wide_clusters(int slices, int *clusters) {
+  static DeviceNumbers<kMaxWideSlices + 1> caps;
+  return caps.get(slices, clusters, [slices](int *n) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * slices, 1, 1);
+    cfg.blockDim = dim3(Wide<BLOCK>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Wide<BLOCK>::kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2 * slices;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(n, wide_kernel<BLOCK>, &cfg);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
   });
-  return cap[slices];
 }
 
 template <typename... Args>
@@ -815,16 +808,18 @@ cudaError_t launch_wide(const MicroGemmArgs &a, MicroParams p, cudaStream_t st) 
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t err = allow_shared(wide_kernel<BLOCK>, Wide<BLOCK>::kSmem, ready);
+  cudaError_t err = allow_shared(wide_kernel<BLOCK>, Wide<BLOCK>::kSmem, ready);
   if (err != cudaSuccess) return err;
-  const int pairs = wide_clusters<BLOCK>(1);
+  int pairs = 0;
+  if ((err = wide_clusters<BLOCK>(1, &pairs)) != cudaSuccess) return err;
   if (pairs < 1) return cudaErrorInvalidConfiguration;
   // few tiles: slices of K over the idle pairs.  A stage takes about 0.4 us
   // and a join about 3 us, as much as 8 stages.
   int s = 1;
   int64_t best = (tiles + pairs - 1) / pairs * p.stages;
   for (int i = 2; i <= kMaxWideSlices && i <= p.stages; ++i) {
-    const int cap = wide_clusters<BLOCK>(i);
+    int cap = 0;
+    if ((err = wide_clusters<BLOCK>(i, &cap)) != cudaSuccess) return err;
     if (cap < 1) break;
     const int64_t cost = (tiles + cap - 1) / cap * ((p.stages + i - 1) / i + 8);
     if (cost < best) best = cost, s = i;

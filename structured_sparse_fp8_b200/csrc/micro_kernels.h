@@ -19,10 +19,30 @@ cudaError_t allow_shared(void (*kernel)(Args...), uint32_t bytes, std::atomic<ui
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
   if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
   return e;
 }
+
+// Numbers that a device has, each asked for once a device; what could not be
+// told is asked for again.
+template <int N>
+struct DeviceNumbers {
+  std::atomic<int> known[64][N] = {};  // the number + 1, or 0
+  template <typename Ask>  // cudaError_t ask(int *)
+  cudaError_t get(int which, int *number, Ask ask) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int> &k = known[dev & 63][which];
+    *number = k.load(std::memory_order_relaxed) - 1;
+    if (*number >= 0) return cudaSuccess;
+    e = ask(number);
+    if (e == cudaSuccess) k.store(*number + 1, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 // ---- rowquant.cu
 enum RowOut : int { kOutE4M3 = 0, kOutNvfp4 = 1, kOutMxfp4 = 2 };

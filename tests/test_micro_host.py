@@ -2,6 +2,8 @@
 against hand-made values and brute force, the sizes and refusals of the C ABI,
 and the refusals of the Python entry points."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -154,6 +156,53 @@ def test_gemm_refuses_sums_whose_stages_pass_an_int(lib):
         assert g(FAKE, FAKE, FAKE, 1, FAKE, FAKE, FAKE, 1, 0, FAKE, 1, 8, k, None, None) == _lib.SP24_ERR_SHAPE
     # the longest sum passes the checks of shapes (and is refused for its alignment here)
     assert g(ODD, FAKE, FAKE, 1, FAKE, FAKE, FAKE, 1, 0, FAKE, 1, 8, (1 << 31) - 256, None, None) == _lib.SP24_ERR_ALIGN
+
+
+DEVICE_STATE = r"""
+#include "micro_kernels.h"
+#include <cstdio>
+static int current = 0, attributes = 0;
+extern "C" cudaError_t cudaGetDevice(int *dev) { *dev = current; return cudaSuccess; }
+extern "C" cudaError_t cudaFuncSetAttribute(const void *, enum cudaFuncAttribute, int) { ++attributes; return cudaSuccess; }
+static void kernel(int) {}
+int main() {
+  static sp24::DeviceNumbers<2> numbers;
+  int asked = 0, n = 0;
+  bool fails = true;
+  auto ask = [&](int *v) { ++asked; *v = 10 * current + (current == 2 ? -20 : 3); return fails ? cudaErrorUnknown : cudaSuccess; };
+  // a failure is reported, and not kept
+  bool ok = numbers.get(0, &n, ask) == cudaErrorUnknown && asked == 1;
+  fails = false;
+  for (int i = 0; i < 3; ++i) ok &= numbers.get(0, &n, ask) == cudaSuccess && n == 3 && asked == 2;
+  // another number and another device are asked for on their own
+  ok &= numbers.get(1, &n, ask) == cudaSuccess && asked == 3;
+  current = 1;
+  ok &= numbers.get(0, &n, ask) == cudaSuccess && n == 13 && asked == 4;
+  current = 2;  // a device that has none: known too
+  for (int i = 0; i < 2; ++i) ok &= numbers.get(0, &n, ask) == cudaSuccess && n == 0 && asked == 5;
+  current = 0;
+  ok &= numbers.get(0, &n, ask) == cudaSuccess && n == 3 && asked == 5;
+  // the allowance of shared memory, likewise once a device
+  static std::atomic<uint64_t> ready{0};
+  for (int d : {0, 1, 0, 1}) {
+    current = d;
+    ok &= sp24::allow_shared(kernel, 65536u, ready) == cudaSuccess;
+  }
+  ok &= attributes == 2;
+  std::puts(ok ? "ok" : "wrong");
+}
+"""
+
+
+def test_what_a_device_is_asked_is_kept_for_each_device(tmp_path):
+    """Against fakes of the CUDA calls: a failed question is asked again, and
+    one device's answer is not another's."""
+    src = tmp_path / "state.cpp"
+    src.write_text(DEVICE_STATE)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(B.nvcc_path())), "include")
+    subprocess.run(["g++", "-std=c++17", "-I", B.CSRC, "-I", B.INCLUDE, "-I", cuda, str(src), "-o", str(tmp_path / "state")],
+                   check=True, capture_output=True, timeout=120)
+    assert subprocess.run([str(tmp_path / "state")], capture_output=True, text=True, timeout=60).stdout == "ok\n"
 
 
 # ------------------------------------------------------------------ Python
