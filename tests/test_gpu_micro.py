@@ -1087,3 +1087,57 @@ def test_product_of_rows_past_32_bit_offsets(fmt, n):
     y = sp().fp4_gemm_microscaled(*w, q, b, s, fmt)
     for lo in (0, 65536, rows - 256, rows - 128):
         check(y[:, lo:lo + 128].t(), lo)
+
+
+def masked(b, rows, cols, fmt, keep):
+    return MO.from_tiles(b.cpu().numpy(), rows, cols // MO.BLOCK[fmt])[keep]
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("stage", ["norm", "norm residual", "gate"])
+@pytest.mark.parametrize("bad", ["inf", "nan", "overflow"])
+@pytest.mark.parametrize("rows,cols", [(5, 96), (900, 2048), (5, 20000 // 32 * 32), (3, 40032)])
+def test_fp4_row_stages_flag_nonfinite_rows_and_keep_the_others(fmt, stage, bad, rows, cols):
+    """One value of a row that is not finite, or whose product (the norm's: its
+    square, or the sum with the residual) leaves its type's range."""
+    m, at = sp(), cols - 3
+    x = WL.random_bits((rows, 2 * cols if stage == "gate" else cols), 8)
+    r = WL.random_bits((rows, cols), 10)
+    w = dev_bf16(WL.random_bits((1, cols), 9)[0])
+
+    def call(x, r, st=None):
+        if stage == "gate":
+            return m.fp4_silu_mul_quantize_microscaled(dev_bf16(x), fmt, status=st)
+        return m.fp4_rmsnorm_quantize_microscaled(dev_bf16(x), w, 1e-5, fmt, status=st,
+                                                  residual=dev_bf16(r) if stage == "norm residual" else None)
+
+    st = status()
+    good = call(x, r, st)
+    assert int(st.item()) == 0
+    x[1, at] = dict(inf=0xFF80, nan=0x7FC0, overflow=0x7F7F)[bad]
+    if bad == "overflow":
+        r[1, at] = 0x7F7F
+        if stage == "gate":
+            x[1, cols + at] = 0x7F00
+    got = call(x, r, st)
+    assert int(st.item()) == m._lib.SP24_STATUS_NONFINITE
+    keep = [0] + list(range(2, rows))
+    assert torch.equal(got[0][keep], good[0][keep])
+    assert np.array_equal(masked(got[1], rows, cols, fmt, keep), masked(good[1], rows, cols, fmt, keep))
+    assert got[2] is None or torch.equal(got[2][keep], good[2][keep])
+    if stage != "gate":
+        assert torch.equal(got[3][keep], good[3][keep])
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("where", ["x", "residual"])
+@pytest.mark.parametrize("rows,cols", [(9, 64), (9, 4096), (700, 4096), (300, 11008), (5, 40032)])
+def test_fp4_norm_in_place(fmt, where, rows, cols):
+    x, r = WL.random_bits((rows, cols), 61), WL.random_bits((rows, cols), 62)
+    w = dev_bf16(WL.random_bits((1, cols), 63)[0])
+    want = sp().fp4_rmsnorm_quantize_microscaled(dev_bf16(x), w, 1e-6, fmt, residual=dev_bf16(r))
+    X, R = dev_bf16(x), dev_bf16(r)
+    target = X if where == "x" else R
+    got = sp().fp4_rmsnorm_quantize_microscaled(X, w, 1e-6, fmt, residual=R, residual_out=target)
+    assert got[3] is target
+    assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
