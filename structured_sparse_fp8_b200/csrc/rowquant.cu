@@ -404,9 +404,10 @@ __device__ __forceinline__ void encode_chunk(const RowQuantArgs &p, const Row &r
     uint32_t word = on ? code << (8 * (lane / lanes & 3)) : 0u;
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, lanes);
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * lanes);
-    // (tiles of a row of 2^28 columns and more pass 32-bit offsets)
+    // (c is a multiple of 4 * lanes here: tile c / (4 lanes), and one 64-bit
+    // product, as tiles of a row of 2^28 columns and more pass 32-bit offsets)
     if (on && lane % (4 * lanes) == 0)
-      *reinterpret_cast<uint32_t *>(row.blocks + static_cast<int64_t>(c / (4 * lanes)) * 512) = word;
+      *reinterpret_cast<uint32_t *>(row.blocks + static_cast<int64_t>(c) * (512 / (4 * lanes))) = word;
   }
 }
 
