@@ -461,7 +461,8 @@ int fp4_unpack_e4m3(const uint8_t *q, int64_t rows, int64_t cols, uint8_t *out, 
  *   Y[m, n] = bf16( x_scale(m) * w_scale(n) * sum_k x[m, k] * w[n, k] ),
  * x and w the values code * block scale, fp32 accumulation, x_scale(m) =
  * x_scales[m] when x_per_token, else x_scales[0], or 1 when x_scales is NULL;
- * w_scale(n) likewise.  Xq u8 [M, K / 2], Wq u8 [N, K / 2], block scales in
+ * w_scale(n) likewise; the two are multiplied first, in fp32, and their product
+ * should be one of its normal numbers.  Xq u8 [M, K / 2], Wq u8 [N, K / 2], block scales in
  * the tiles above (E4M3 ones without a sign; what the tiles hold outside the
  * matrix does not matter), of [M, K] and [N, K].  Products below 2^-126 may
  * count as zero.  Y bf16 [M, N] must not alias an
@@ -508,8 +509,10 @@ int fp4_rmsnorm_quantize_microscaled(const void *X, const void *residual, const 
  * The gated activation between the two products of a feed-forward block, with
  * a quantised output.  GU bf16 [rows, 2 cols] holds the gate's columns, then
  * the up projection's (one GEMM over both weights stacked); y = g / (1 +
- * exp(-g)) * u in fp32 (1 / (1 + exp(-g)) below 2^-130 counts as 0), quantised
- * as by the norm's two forms.  Shape rules, status and outputs as there.
+ * exp(-g)) * u in fp32 (within (1.2 |g| + 8) * 2^-23 of itself, as the
+ * exponential's argument is one fp32 product; 1 / (1 + exp(-g)) below 2^-130
+ * counts as 0), quantised as by the norm's two forms.  Shape rules, status and
+ * outputs as there.
  */
 int fp8_silu_mul_quantize_pertoken(const void *GU, int64_t rows, int64_t cols, uint8_t *q, float *scales,
                                    int32_t *status, sp24_stream_t stream);

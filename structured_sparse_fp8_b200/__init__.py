@@ -775,7 +775,8 @@ def fp4_gemm_microscaled(xq: torch.Tensor, x_block_scales: torch.Tensor, x_scale
                          w_block_scales: torch.Tensor, w_scales, format: str = "nvfp4",
                          out: torch.Tensor | None = None, status: torch.Tensor | None = None):
     """Y bf16 [M, N] = x . w^T of two block-scaled FP4 matrices: xq u8 [M, K/2] and
-    wq u8 [N, K/2] with the block scales of fp4_quantize_microscaled; x_scales
+    wq u8 [N, K/2] with the block scales of fp4_quantize_microscaled (all as
+    uint8: tensors of an 8-bit float type by .view(torch.uint8)); x_scales
     and w_scales hold one value per row, one for all, or are None (1)."""
     code, block = _fp4_format(format)
     if xq.dtype != _U8 or xq.dim() != 2 or wq.dim() != 2:

@@ -19,20 +19,22 @@
 //     (128 rows), the tokens its B operand (BN columns), one CTA per tile and K
 //     slice.  Such calls stream the weights, so K is sliced over a cluster of
 //     CTAs until the SMs are full; the slices' partial sums meet in shared
-//     memory over the cluster (distributed shared memory), are added in slice
-//     order and written once.
+//     memory over the cluster (distributed shared memory), are added in a fixed
+//     order (the owner's, then the others by slice) and written once.
 //     Bound by latency next to the weights' bytes: the start, the ring's first
 //     fill and the join (1 x 11008 x 4096 takes 6.0 us of its 7.2 with all
 //     operands in L2).
 //   wide (more tokens): an SM pair (cta_group::2) multiplies 256 tokens by 256
 //     weight rows, so that each SM reads half of both operands.  Bound by the
-//     tensor pipe (a stage's 256 x 256 x 256 products take 0.37 us of its 0.4
-//     at four times the measured bf16 rate), in long calls at the clock that
-//     the power limit leaves, and in calls of few tiles by the join of K slices
-//     (3 us) and the idle pairs.
-// Measured, nvfp4, cold operands: 1 x 11008 x 4096 7.2 us (3.5 TB/s), 64 x 11008
-// x 4096 9.7, 256 x 4096 x 14336 16.5 (1.8 PFLOP/s), 2048 x 4096 x 4096 18.3
-// (3.8), 4096 x 12288 x 4096 85 (4.9); mxfp4, half the scales, 0 to 10 % less.
+//     tensor pipe (a stage's 256 x 256 x 256 products would take 0.37 us of its
+//     0.4 at four times the measured bf16 rate; no FP4 rate is measured), in
+//     long runs at the clock that the power limit leaves, and in calls of few
+//     tiles by the join of K slices (3 us) and the idle pairs.
+// Measured, nvfp4, cold operands: 1 x 11008 x 4096 7.3 us (3.5 TB/s), 64 x 11008
+// x 4096 9.7, 256 x 4096 x 14336 16.6 (1.8 PFLOP/s), 2048 x 4096 x 4096 18.1
+// (3.8), 4096 x 12288 x 4096 86 (4.8) from a cool start and 100 (4.1) after
+// seconds of it, at 1490 MHz under the power limit; mxfp4, half the scales, 2 to
+// 8 % less.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -107,10 +109,11 @@ __device__ __forceinline__ void bulk_push(uint32_t dst, const void *src, uint32_
                : "memory");
 }
 
-// The CTAs of a cluster order only each other's asynchronous operations here
-// (tensor-memory reads that have returned, bulk copies counted on mbarriers,
-// mbarriers whose initialisation is fenced), never plain stores, so their
-// arrivals are relaxed: a release at cluster scope first waits for the
+// The CTAs of a cluster order only each other's asynchronous operations here,
+// never plain stores: tensor-memory reads that have returned (wait::ld) and that
+// the tcgen05 fences before the arrival and behind the wait order around it;
+// bulk copies counted on mbarriers; mbarriers whose initialisation is fenced.
+// So their arrivals are relaxed: a release at cluster scope first waits for the
 // thread's earlier stores, which took 0.6 to 0.7 us of every tile of Y.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -144,8 +147,8 @@ struct MicroParams {
 // tokens [i * per, (i + 1) * per); every slice lays its fp32 sums out [token]
 // [128 rows], copies each other owner's tokens into that CTA (one bulk copy
 // each: plain stores into another CTA's shared memory moved about 5 bytes/ns
-// per SM, which made a 128 x 256 tile's join 20 us), and the owner adds them,
-// slices in order.  Up to 32 tokens what arrives has room of its own; wider
+// per SM, which made a 128 x 256 tile's join 20 us), and the owner adds them to
+// its own, slices in order.  Up to 32 tokens what arrives has room of its own; wider
 // tiles take it over the ring, once every CTA has finished its main loop.
 
 // Tokens that arrive from other slices at most: (slices - 1) * ceil(BN / slices).

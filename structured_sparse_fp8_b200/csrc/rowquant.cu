@@ -32,9 +32,9 @@
 // nvfp4, 12288 x 4096, 29.3 us against 23.9.  Rows brought ahead into shared
 // memory by bulk copies of CTAs that stay: norm 43 us against 35 at 4096 x
 // 8192.)  Measured with cold inputs, bytes read and written over the time:
-// norm to E4M3, 4096 x 4096, 18.9 us (6.2 TB/s), 1 x 4096 1.9 us; gate to
+// norm to E4M3, 4096 x 4096, 18.9 us (6.2 TB/s), 1 x 4096 1.8 us; gate to
 // mxfp4, 4096 x 14336, 39.8 us (6.7 TB/s); quantiser, 12288 x 4096, to mxfp4
-// 20.2 us (6.3 TB/s), to nvfp4 23.9 (5.4).
+// 20.4 us (6.3 TB/s), to nvfp4 23.9 (5.4).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -221,9 +221,13 @@ __device__ __forceinline__ Chunk norm_values(const Raw &h, const Raw &w, f2 &sum
   return y;
 }
 
-// g / (1 + exp(-g)) * u.  The reciprocal is taken of (1 + exp(-g)) / 16, so that
-// neither leaves the range of normal numbers while the factor is at least
-// 2^-130 (below that, from g = -90.1 on, it counts as 0): u may be large.
+// g / (1 + exp(-g)) * u.  The exponential's argument is one fp32 product, so
+// the result is within (1.173 |g| + 8) * 2^-23 of itself.  Codes have 3 bits at
+// most, and no more of them differ from the exact value's than with a library's
+// exponential (E4M3, 8.4 million normal values: 14 and 14).  The reciprocal is
+// taken of (1 + exp(-g)) / 16, so that neither leaves the range of normal
+// numbers while the factor is at least 2^-130 (below that, from g = -90.1 on, it
+// counts as 0): u may be large.
 __device__ __forceinline__ Chunk gate_values(const Raw &gv, const Raw &uv) {
   Chunk g = unpack(gv);
   const Chunk u = unpack(uv);
@@ -290,6 +294,7 @@ struct RowScale {
   float mul;   // E4M3: codes are E4M3(value * mul); nvfp4: 2688 / R; mxfp4: rstd
   float sf;    // nvfp4: block scales are E4M3(amax * sf), sf = 448 / R
 };
+// 1 / v: the approximation and one Newton step
 __device__ __forceinline__ float rcp_refined(float v) {
   const float r = rcp_approx(v);
   return fmaf(r, fmaf(-v, r, 1.0f), r);
@@ -334,7 +339,10 @@ __device__ __forceinline__ float stored_scale(float top) {  // top = amax * rstd
 // the values have few significant bits, are either on a rounding boundary of
 // the code or well away from it; computed to 2^-21.5 of themselves, they are
 // first rounded to fewer bits, which moves them onto the boundary, so that ties
-// are decided as for the exact quotient.
+// are decided as for the exact quotient.  That is done for plain values' block
+// scales and codes and for the norm's block scales.  The norm's codes (z has 16
+// bits; about 1.6 of 4096 quotients are ties) and all of the gate's quotients are
+// rounded as fp32 gives them.
 // Block scales, 448 amax_b / R: 17 bits for plain values (at least 2^-13 from a
 // boundary otherwise), 22 for the norm's z (16 bits; 2^-20).
 template <int SRC>
